@@ -13,6 +13,7 @@ value-embedding residual v + 3*sigmoid(gate)*ve.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from dataclasses import dataclass
 
@@ -32,7 +33,9 @@ F32, BF16 = 0, 1
 EXPORTS = ("attn_prologue", "attn_prologue_gated", "attn_gate_bwd", "attn_qkv_prologue",
            "attn_qkv_fp8_workspace_bytes", "attn_qkv_prologue_fp8", "attn_qkv_bwd", "attn_fwd",
            "attn_bwd_workspace_bytes", "attn_bwd", "attn_bwd_noalloc",
-           "attn_decode_workspace_bytes", "attn_decode", "cswattn_gemm_bf16",
+           "attn_decode_workspace_bytes", "attn_decode", "attn_paged_append",
+           "attn_paged_workspace_bytes", "attn_paged", "attn_paged_weigh", "attn_paged_select",
+           "attn_paged_move", "cswattn_gemm_bf16",
            "muon_ns_workspace_bytes", "muon_newton_schulz",
            "cswattn_sync_status", "cswattn_set_wait_limit_ns", "cswattn_set_timing",
            "cswattn_kernel_times", "cswattn_selftest_wait_timeout", "cswattn_last_error",
@@ -47,6 +50,19 @@ class CswattnLayer(ctypes.Structure):
         ("rope_base", ctypes.c_float), ("eps", ctypes.c_float), ("softmax_scale", ctypes.c_float),
         ("has_ve", ctypes.c_int), ("dtype", ctypes.c_int),
     ]
+
+
+class CswattnPaged(ctypes.Structure):
+    _fields_ = [
+        ("page_size", ctypes.c_int), ("n_pages", ctypes.c_int), ("pages_per_seq", ctypes.c_int),
+        ("n_tokens", ctypes.c_int), ("max_new", ctypes.c_int), ("page_table", ctypes.c_void_p),
+        ("cache_len", ctypes.c_void_p), ("new_start", ctypes.c_void_p),
+    ]
+
+
+class CswattnRope(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int), ("interleaved", ctypes.c_int), ("factor", ctypes.c_float),
+                ("frequencies", ctypes.POINTER(ctypes.c_double))]
 
 
 class CswattnError(RuntimeError):
@@ -106,6 +122,17 @@ def lib():
         L.attn_decode_workspace_bytes.argtypes = [lp]
         L.attn_decode_workspace_bytes.restype = sz
         L.attn_decode.argtypes = [lp] + [vp] * 5 + [vp, vp, vp, vp, fp, vp, sz, vp]
+        pp, rp = ctypes.POINTER(CswattnPaged), ctypes.POINTER(CswattnRope)
+        L.attn_paged_append.argtypes = [lp, pp, rp] + [vp] * 12
+        L.attn_paged_workspace_bytes.argtypes = [lp, pp]
+        L.attn_paged_workspace_bytes.restype = sz
+        L.attn_paged.argtypes = [lp, pp] + [vp] * 6 + [sz, vp]
+        L.attn_paged_weigh.argtypes = [lp, pp] + [vp] * 5
+        L.attn_paged_select.argtypes = [lp, pp] + [vp] * 3 + [ci, ci] + [vp] * 5
+        L.attn_paged_move.argtypes = [lp, pp] + [vp] * 3 + [ci] + [vp] * 5
+        for name in ("attn_paged_append", "attn_paged", "attn_paged_weigh", "attn_paged_select",
+                     "attn_paged_move"):
+            getattr(L, name).restype = ci
         for name in ("attn_prologue", "attn_prologue_gated", "attn_gate_bwd", "attn_fwd", "attn_bwd",
                      "attn_bwd_noalloc", "cswattn_sync_status"):
             getattr(L, name).restype = ctypes.c_int
@@ -275,6 +302,235 @@ def attn_decode(spec: LayerSpec, q, k, v, ve, gate, cache_len, k_cache, v_cache,
     _check(lib().attn_decode(ctypes.byref(layer), _ptr(q), _ptr(k), _ptr(v), _ptr(ve), _ptr(gate),
                              _ptr(cache_len), _ptr(k_cache), _ptr(v_cache), _ptr(O), _ptr(lse),
                              _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+# ------------------------------------------------------------------ paged cache
+
+class RopeSpec:
+    """Rotary positions of attn_paged_append: the layout (halves, or pairs of
+    neighbours when interleaved), how much of the head turns, and the
+    frequencies of a stretched context:
+
+    "none"     base^(-2i/R)
+    "linear"   the same, divided by ``factor`` (positions interpolated)
+    "ntk"      base * factor^(R/(R-2)) in the place of base
+    "yarn"     pairs that turn more than ``beta_fast`` times within
+               ``original_length`` positions as they are, those below
+               ``beta_slow`` turns divided by ``factor``, a ramp between, and
+               cos and sin times 0.1 ln(factor) + 1
+
+    or ``frequencies``: one angle per position for each pair, in their place.
+    ``attention_factor`` replaces the factor on cos and sin.
+    """
+
+    SCALINGS = ("none", "linear", "ntk", "yarn")
+
+    def __init__(self, rotary_dim, interleaved=False, scaling="none", factor=1.0, base=10000.0,
+                 original_length=None, beta_fast=32.0, beta_slow=1.0, attention_factor=None, frequencies=None):
+        R = int(rotary_dim)
+        if R < 2 or R % 2:
+            raise ValueError(f"rotary_dim must be even and >= 2, got {rotary_dim}")
+        if scaling not in self.SCALINGS:
+            raise ValueError(f"scaling must be one of {self.SCALINGS}, got {scaling!r}")
+        if not (math.isfinite(factor) and factor > 0) or not (math.isfinite(base) and base > 0):
+            raise ValueError("factor and base must be finite and > 0")
+        scale = 1.0
+        if frequencies is not None:
+            w = [float(f) for f in frequencies]
+            if len(w) != R // 2:
+                raise ValueError(f"{R // 2} frequencies are wanted, got {len(w)}")
+        else:
+            if scaling == "ntk":
+                if R == 2:
+                    raise ValueError("ntk scaling needs rotary_dim > 2")
+                base = base * factor ** (R / (R - 2))
+            w = [base ** (-2.0 * i / R) for i in range(R // 2)]
+            if scaling == "linear":
+                w = [f / factor for f in w]
+            elif scaling == "yarn":
+                if not original_length or base == 1.0:
+                    raise ValueError("yarn scaling needs original_length and a base other than 1")
+
+                def pair_of(turns):  # the pair that turns this often within original_length
+                    return R * math.log(original_length / (turns * 2 * math.pi)) / (2 * math.log(base))
+                low = max(math.floor(pair_of(beta_fast)), 0)
+                high = min(math.ceil(pair_of(beta_slow)), R // 2 - 1)
+                for i in range(R // 2):
+                    ramp = min(max((i - low) / max(high - low, 0.001), 0.0), 1.0)
+                    w[i] = w[i] * (1 - ramp) + w[i] / factor * ramp
+                scale = 0.1 * math.log(factor) + 1.0
+        self.rotary_dim, self.interleaved, self.frequencies = R, bool(interleaved), tuple(w)
+        self.attention_factor = float(scale if attention_factor is None else attention_factor)
+        self._freq = (ctypes.c_double * len(w))(*w)
+        self._c = CswattnRope(R, int(self.interleaved), self.attention_factor, self._freq)
+
+
+class PagedCache:
+    """The pools of a paged cache: k and v (n_pages, page_size, n_kv_head,
+    head_dim) bf16 and, for eviction, weight (float32) and position (int32),
+    (n_pages, n_kv_head, page_size). Allocates them (weight and position only
+    with track_weights), or takes the tensors given."""
+
+    def __init__(self, spec: LayerSpec, n_pages=None, page_size=None, track_weights=False, k=None, v=None,
+                 weight=None, position=None, device="cuda"):
+        import torch
+        if n_pages is not None:
+            kv, term = (n_pages, page_size, spec.n_kv_head, spec.head_dim), (n_pages, spec.n_kv_head, page_size)
+            k = torch.empty(*kv, device=device, dtype=torch.bfloat16) if k is None else k
+            v = torch.empty(*kv, device=device, dtype=torch.bfloat16) if v is None else v
+            if track_weights:
+                weight = torch.zeros(*term, device=device) if weight is None else weight
+                position = torch.zeros(*term, device=device, dtype=torch.int32) if position is None else position
+        if k is not None:
+            n_pages, page_size = k.shape[0], k.shape[1]
+        elif weight is not None:
+            n_pages, page_size = weight.shape[0], weight.shape[2]
+        else:
+            raise ValueError("PagedCache needs n_pages and page_size, or the pools")
+        kv, term = (n_pages, page_size, spec.n_kv_head, spec.head_dim), (n_pages, spec.n_kv_head, page_size)
+        for name, t, shape, dtype in (("k", k, kv, torch.bfloat16), ("v", v, kv, torch.bfloat16),
+                                      ("weight", weight, term, torch.float32),
+                                      ("position", position, term, torch.int32)):
+            if t is not None:
+                _want(name, t, shape, dtype)
+        self.k, self.v, self.weight, self.position = k, v, weight, position
+        self.n_pages, self.page_size = n_pages, page_size
+
+
+class PagedBatch:
+    """The sequences of a paged call: page_table (B, pages_per_seq), cache_len
+    (B) and new_start (B + 1), int32 device tensors; n_tokens rows of q, and
+    the most new tokens a sequence has (new_start, n_tokens and max_new are
+    not needed to select and move rows)."""
+
+    def __init__(self, page_table, cache_len, new_start=None, n_tokens=0, max_new=0):
+        import torch
+        B, pages = page_table.shape
+        _want("page_table", page_table, (B, pages), torch.int32)
+        _want("cache_len", cache_len, (B,), torch.int32)
+        if new_start is not None:
+            _want("new_start", new_start, (B + 1,), torch.int32)
+        self.page_table, self.cache_len, self.new_start = page_table, cache_len, new_start
+        self.n_tokens, self.max_new = int(n_tokens), int(max_new)
+
+    def c(self, spec: LayerSpec, cache: PagedCache) -> CswattnPaged:
+        B, pages = self.page_table.shape
+        if B != spec.B:
+            raise ValueError(f"the batch has {B} sequences, the layer {spec.B}")
+        return CswattnPaged(cache.page_size, cache.n_pages, pages, self.n_tokens, self.max_new,
+                            self.page_table.data_ptr(), self.cache_len.data_ptr(),
+                            None if self.new_start is None else self.new_start.data_ptr())
+
+
+def _want(name, t, shape, dtype):
+    if t is None:
+        raise ValueError(f"{name} is needed")
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _same_device(batch: PagedBatch, *tensors):
+    """All tensors of a paged call lie on the page table's device; the call
+    is made with that device current (its context is the one the kernels are
+    launched in)."""
+    import torch
+    device = batch.page_table.device
+    for t in (batch.cache_len, batch.new_start, *tensors):
+        if t is not None and t.device != device:
+            raise ValueError(f"tensors of a paged call lie on {device} and {t.device}")
+    return torch.cuda.device(device)
+
+
+def attn_paged_append(spec: LayerSpec, batch: PagedBatch, cache: PagedCache, q, k, v, ve, gate, q_out,
+                      positions=None, rope: RopeSpec | None = None, stream=None):
+    """The prologue of the batch's new tokens: q_out, and their rows of the
+    cache. rope None: the layer's plain RoPE."""
+    import torch
+    N, H, Hk, D = batch.n_tokens, spec.n_head, spec.n_kv_head, spec.head_dim
+    bf = torch.bfloat16
+    for name, t, shape in (("q", q, (N, H, D)), ("k", k, (N, Hk, D)), ("v", v, (N, Hk, D)), ("q_out", q_out, (N, H, D))):
+        _want(name, t, shape, bf)
+    if spec.has_ve:
+        _want("ve", ve, (N, Hk, D), bf)
+        _want("gate", gate, (N, Hk), bf)
+    if positions is not None:
+        _want("positions", positions, (N,), torch.int32)
+    layer, paged = spec.c(), batch.c(spec, cache)
+    with _same_device(batch, q, k, v, ve, gate, q_out, positions, cache.k, cache.v, cache.weight, cache.position):
+        _check(lib().attn_paged_append(ctypes.byref(layer), ctypes.byref(paged),
+                                       None if rope is None else ctypes.byref(rope._c), _ptr(q), _ptr(k), _ptr(v),
+                                       _ptr(ve), _ptr(gate), _ptr(positions), _ptr(q_out), _ptr(cache.k),
+                                       _ptr(cache.v), _ptr(cache.weight), _ptr(cache.position), _stream(stream)))
+
+
+def attn_paged_workspace_bytes(spec: LayerSpec, batch: PagedBatch, cache: PagedCache) -> int:
+    """Scratch bytes of attn_paged for this layer and the batch's sizes."""
+    layer, paged = spec.c(), batch.c(spec, cache)
+    return int(lib().attn_paged_workspace_bytes(ctypes.byref(layer), ctypes.byref(paged)))
+
+
+def attn_paged(spec: LayerSpec, batch: PagedBatch, cache: PagedCache, q_out, O, lse, workspace,
+               workspace_bytes=None, stream=None):
+    """Attention of the new tokens (q_out of attn_paged_append) over the
+    cache: O (n_tokens, H, D) and lse (n_tokens, H)."""
+    import torch
+    N, H, D = batch.n_tokens, spec.n_head, spec.head_dim
+    _want("q_out", q_out, (N, H, D), torch.bfloat16)
+    _want("O", O, (N, H, D), torch.bfloat16)
+    _want("lse", lse, (N, H), torch.float32)
+    layer, paged = spec.c(), batch.c(spec, cache)
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    with _same_device(batch, q_out, O, lse, workspace, cache.k, cache.v):
+        _check(lib().attn_paged(ctypes.byref(layer), ctypes.byref(paged), _ptr(q_out), _ptr(cache.k), _ptr(cache.v),
+                                _ptr(O), _ptr(lse), _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def attn_paged_weigh(spec: LayerSpec, batch: PagedBatch, cache: PagedCache, q_out, lse, stream=None):
+    """Adds the new tokens' attention weights to cache.weight."""
+    import torch
+    N, H, D = batch.n_tokens, spec.n_head, spec.head_dim
+    _want("q_out", q_out, (N, H, D), torch.bfloat16)
+    _want("lse", lse, (N, H), torch.float32)
+    layer, paged = spec.c(), batch.c(spec, cache)
+    with _same_device(batch, q_out, lse, cache.k, cache.weight):
+        _check(lib().attn_paged_weigh(ctypes.byref(layer), ctypes.byref(paged), _ptr(q_out), _ptr(cache.k),
+                                      _ptr(lse), _ptr(cache.weight), _stream(stream)))
+
+
+def attn_paged_select(spec: LayerSpec, batch: PagedBatch, cache: PagedCache, next_pos, n_keep, n_recent, n_moves,
+                      src, dst, new_len, stream=None):
+    """Which rows each KV head keeps under a budget of n_keep rows, as moves
+    (src, dst) of n_moves rows, and the sequences' new lengths."""
+    import torch
+    B, Hk = spec.B, spec.n_kv_head
+    i32 = torch.int32
+    for name, t, shape in (("next_pos", next_pos, (B,)), ("n_moves", n_moves, (B, Hk)), ("src", src, (B, Hk, n_keep)),
+                           ("dst", dst, (B, Hk, n_keep)), ("new_len", new_len, (B,))):
+        _want(name, t, shape, i32)
+    layer, paged = spec.c(), batch.c(spec, cache)
+    with _same_device(batch, next_pos, n_moves, src, dst, new_len, cache.weight, cache.position):
+        _check(lib().attn_paged_select(ctypes.byref(layer), ctypes.byref(paged), _ptr(cache.weight),
+                                       _ptr(cache.position), _ptr(next_pos), int(n_keep), int(n_recent),
+                                       _ptr(n_moves), _ptr(src), _ptr(dst), _ptr(new_len), _stream(stream)))
+
+
+def attn_paged_move(spec: LayerSpec, batch: PagedBatch, cache: PagedCache, n_moves, src, dst, stream=None):
+    """Moves the kept rows of attn_paged_select to their new places."""
+    import torch
+    B, Hk, n_keep = src.shape
+    _want("n_moves", n_moves, (spec.B, spec.n_kv_head), torch.int32)
+    _want("src", src, (spec.B, spec.n_kv_head, n_keep), torch.int32)
+    _want("dst", dst, (spec.B, spec.n_kv_head, n_keep), torch.int32)
+    layer, paged = spec.c(), batch.c(spec, cache)
+    with _same_device(batch, n_moves, src, dst, cache.k, cache.v, cache.weight, cache.position):
+        _check(lib().attn_paged_move(ctypes.byref(layer), ctypes.byref(paged), _ptr(n_moves), _ptr(src), _ptr(dst),
+                                     int(n_keep), _ptr(cache.k), _ptr(cache.v), _ptr(cache.weight),
+                                     _ptr(cache.position), _stream(stream)))
 
 
 def cswattn_sync_status(stream=None):

@@ -26,6 +26,9 @@
 #include "gemm_sm100.cuh"
 #include "qkv_sm100.cuh"
 #include "fp8.cuh"
+#include "paged_append.cuh"
+#include "paged_simple.cuh"
+#include "paged_evict.cuh"
 
 using namespace cswattn;
 
@@ -766,7 +769,7 @@ cswattn_status launch_decode(const Shape& s, const CUtensorMap& mk, const CUtens
 
 extern "C" {
 
-int cswattn_version(void) { return (1 << 16) | 0; }
+int cswattn_version(void) { return (1 << 16) | 1; }
 
 const char* cswattn_last_error(void) { return t_err.c_str(); }
 
@@ -822,7 +825,8 @@ cswattn_status cswattn_sync_status(void* stream) {
       return fail(CSWATTN_ERR_BOUNDS, "a device-side bounds check failed; the access was skipped (status 0x%x)", v);
     if (v & kStatusTimeout) return fail(CSWATTN_ERR_TIMEOUT, "a device-side wait ran out (status 0x%x)", v);
     if (v & kStatusRange)
-      return fail(CSWATTN_ERR_INVALID_ARG, "a decode step met a cache length outside [0, T) (status 0x%x)", v);
+      return fail(CSWATTN_ERR_INVALID_ARG, "a decode step met a cache length outside [0, T), or a paged call lengths, pages or moves that do not "
+                  "fit it (status 0x%x)", v);
   }
   return CSWATTN_OK;
 }
@@ -1597,3 +1601,5 @@ cswattn_status attn_bwd_noalloc(const cswattn_layer* layer, const void* q, const
 }
 
 }  // extern "C"
+
+#include "paged_api.cuh"

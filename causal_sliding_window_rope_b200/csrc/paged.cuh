@@ -1,0 +1,70 @@
+// paged.cuh -- what the paged-cache kernels share: the batch as the device
+// sees it, the lookup of a token's sequence and of a row's page.
+//
+// Page "5만원으로 나만의 ChatGPT 훈련하는 방법", section "6. 추론 엔진
+// (nanochat/engine.py)": generation over a pre-filled KV cache. Here the
+// cache rows of a sequence lie in pages of `page_size` rows, in any order of
+// pages, and a call takes any number of new tokens per sequence.
+//
+// Sequence b has L = cache_len[b] rows before the call and the tokens
+// new_start[b] .. new_start[b + 1] of the call; token i of it is row L + i.
+// The lengths live on the device, so the host cannot check them: each kernel
+// checks a sequence before it touches it (seq_load) and reports one that does
+// not fit through the status word; such a sequence is left alone.
+#pragma once
+#include "prologue.cuh"
+#include "decode.cuh"
+
+namespace cswattn {
+namespace paged {
+
+constexpr int kMaxSeqs = 4096;   // sequences of one call (the kernels scan their lengths)
+constexpr int kUnit = 16;        // rows: a page holds whole units, so a unit never straddles pages
+
+struct View {
+  int B, T, H, Hk, g, W;
+  int page_size, n_pages, pages_per_seq;
+  int n_tokens, max_new;
+  const int *page_table, *cache_len, *new_start;
+};
+
+struct Seq {
+  int L, n, tok0;  // rows before the call, new tokens, first of them
+};
+
+// False (and reported, by the thread that `report` selects) when the lengths
+// of sequence b do not fit the call; the sequence then counts as empty.
+__device__ __forceinline__ bool seq_load(const View& v, int b, bool report, Seq& s) {
+  s.L = v.cache_len[b];
+  s.tok0 = v.new_start[b];
+  const int end = v.new_start[b + 1];
+  const bool ok = s.L >= 0 && s.tok0 >= 0 && end >= s.tok0 && end <= v.n_tokens && end - s.tok0 <= v.max_new &&
+                  s.L <= v.T - (end - s.tok0);
+  s.n = ok ? end - s.tok0 : 0;
+  if (!ok) {
+    s.L = 0;
+    if (report) atomicOr(&g_status, kStatusRange);
+  }
+  return ok;
+}
+
+// Page of a row of sequence b; -1 (and reported) when the table's entry is
+// not a page of the pool. row < T <= pages_per_seq * page_size.
+__device__ __forceinline__ int page_at(const View& v, int b, int entry) {
+  const int p = v.page_table[static_cast<size_t>(b) * v.pages_per_seq + entry];
+  if (p >= 0 && p < v.n_pages) return p;
+  atomicOr(&g_status, kStatusRange);
+  return -1;
+}
+
+// Row of a (pages, page_size, Hk) pool of K or V rows (in units of head_dim
+// elements) and of a (pages, Hk, page_size) pool of row terms.
+__device__ __forceinline__ size_t kv_index(const View& v, int page, int slot, int hk) {
+  return (static_cast<size_t>(page) * v.page_size + slot) * v.Hk + hk;
+}
+__device__ __forceinline__ size_t term_index(const View& v, int page, int slot, int hk) {
+  return (static_cast<size_t>(page) * v.Hk + hk) * v.page_size + slot;
+}
+
+}  // namespace paged
+}  // namespace cswattn

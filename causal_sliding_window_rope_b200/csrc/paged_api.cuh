@@ -1,0 +1,295 @@
+// paged_api.cuh -- C ABI of the paged cache: host-side validation and
+// launches. Included by cswattn.cu, whose helpers it uses.
+#pragma once
+
+namespace {
+
+constexpr int kMaxPagedGroup = 128;  // query heads per KV head: one token's rows fit one tile
+
+// Checks the layer and the batch's sizes; needs_tokens: the call reads the
+// new tokens (n_tokens, max_new, new_start).
+cswattn_status check_paged(const cswattn_layer* layer, const cswattn_paged* pg, bool needs_tokens, Shape* s,
+                           paged::View* v) {
+  if (!layer) return fail(CSWATTN_ERR_INVALID_ARG, "layer is NULL");
+  if (!pg) return fail(CSWATTN_ERR_INVALID_ARG, "paged is NULL");
+  if (layer->B < 1) return fail(CSWATTN_ERR_INVALID_ARG, "B must be >= 1");
+  cswattn_layer one = *layer;  // T is a bound on each sequence, not B dense ones
+  one.B = 1;
+  cswattn_status st = check_layer(&one, s);
+  if (st != CSWATTN_OK) return st;
+  s->B = layer->B;
+  if (!s->bf16) return fail(CSWATTN_ERR_UNSUPPORTED, "the paged cache supports bf16 layers only");
+  if (s->g > kMaxPagedGroup)
+    return fail(CSWATTN_ERR_UNSUPPORTED, "the paged cache supports up to %d query heads per KV head (got %d)",
+                kMaxPagedGroup, s->g);
+  if (s->B > paged::kMaxSeqs)
+    return fail(CSWATTN_ERR_UNSUPPORTED, "the paged cache supports up to %d sequences (got %d)", paged::kMaxSeqs,
+                s->B);
+  if (pg->page_size < 1 || pg->n_pages < 1 || pg->pages_per_seq < 1)
+    return fail(CSWATTN_ERR_INVALID_ARG, "page_size, n_pages and pages_per_seq must be >= 1");
+  if (pg->page_size % paged::kUnit != 0)
+    return fail(CSWATTN_ERR_UNSUPPORTED, "page_size must be a multiple of %d (got %d)", paged::kUnit,
+                pg->page_size);
+  if (static_cast<long long>(pg->pages_per_seq) * pg->page_size < s->T)
+    return fail(CSWATTN_ERR_INVALID_ARG, "T = %d rows do not fit %d pages of %d", s->T, pg->pages_per_seq,
+                pg->page_size);
+  // The pools' byte strides are those of a tensor map (below 2^40).
+  if (static_cast<double>(pg->page_size) * s->Hk * s->D >= 5e11)
+    return fail(CSWATTN_ERR_UNSUPPORTED, "page too large");
+  CHECK_PTR(pg->page_table, 4);
+  CHECK_PTR(pg->cache_len, 4);
+  if (needs_tokens) {
+    CHECK_PTR(pg->new_start, 4);
+    if (pg->n_tokens < 0) return fail(CSWATTN_ERR_INVALID_ARG, "n_tokens must be >= 0 (got %d)", pg->n_tokens);
+    if (pg->max_new < 1 || pg->max_new > s->T)
+      return fail(CSWATTN_ERR_INVALID_ARG, "max_new must be in [1, T = %d] (got %d)", s->T, pg->max_new);
+  }
+  v->B = s->B;
+  v->T = s->T;
+  v->H = s->H;
+  v->Hk = s->Hk;
+  v->g = s->g;
+  v->W = s->W;
+  v->page_size = pg->page_size;
+  v->n_pages = pg->n_pages;
+  v->pages_per_seq = pg->pages_per_seq;
+  v->n_tokens = pg->n_tokens;
+  v->max_new = pg->max_new;
+  v->page_table = pg->page_table;
+  v->cache_len = pg->cache_len;
+  v->new_start = pg->new_start;
+  return CSWATTN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+cswattn_status attn_paged_append(const cswattn_layer* layer, const cswattn_paged* paged, const cswattn_rope* rope,
+                                 const void* q, const void* k, const void* v, const void* ve, const void* gate,
+                                 const int* positions, void* q_out, void* k_pages, void* v_pages, float* weight,
+                                 int* position, void* stream) {
+  const NvtxRange nvtx_range("attn_paged_append");
+  Shape s;
+  paged::AppendParams ap;
+  cswattn_status st = check_paged(layer, paged, true, &s, &ap.v);
+  if (st != CSWATTN_OK) return st;
+  ap.rotary_pairs = s.D / 2;
+  ap.factor = 1.f;
+  bool interleaved = false;
+  const double* freq = nullptr;
+  if (rope) {
+    if (rope->rotary_dim < 1 || rope->rotary_dim > s.D || (rope->interleaved != 0 && rope->interleaved != 1))
+      return fail(CSWATTN_ERR_INVALID_ARG, "rotary_dim must be in [1, head_dim], interleaved 0 or 1");
+    if (rope->rotary_dim % 16 != 0)
+      return fail(CSWATTN_ERR_UNSUPPORTED, "rotary_dim must be a multiple of 16 (got %d)", rope->rotary_dim);
+    if (!(rope->factor > 0.f) || !std::isfinite(rope->factor))
+      return fail(CSWATTN_ERR_INVALID_ARG, "rope factor must be finite and > 0");
+    ap.rotary_pairs = rope->rotary_dim / 2;
+    ap.factor = rope->factor;
+    interleaved = rope->interleaved != 0;
+    freq = rope->frequencies;
+  }
+  for (int i = 0; i < ap.rotary_pairs; ++i) {
+    const double w = freq ? freq[i] : std::pow(static_cast<double>(layer->rope_base), -1.0 * i / ap.rotary_pairs);
+    if (!std::isfinite(w)) return fail(CSWATTN_ERR_INVALID_ARG, "rope frequency %d is not finite", i);
+    ap.turns[i] = w / 6.283185307179586476925;
+  }
+  if (paged->n_tokens == 0) return CSWATTN_OK;
+  CHECK_PTR(q, 16);
+  CHECK_PTR(k, 16);
+  CHECK_PTR(v, 16);
+  CHECK_PTR(q_out, 16);
+  CHECK_PTR(k_pages, 16);
+  CHECK_PTR(v_pages, 16);
+  if (layer->has_ve) {
+    CHECK_PTR(ve, 16);
+    CHECK_PTR(gate, 2);
+  }
+  if (positions) CHECK_PTR(positions, 4);
+  if ((weight == nullptr) != (position == nullptr))
+    return fail(CSWATTN_ERR_INVALID_ARG, "weight and position must be given both or neither");
+  if (weight) {
+    CHECK_PTR(weight, 4);
+    CHECK_PTR(position, 4);
+  }
+  if (k_pages == v_pages) return fail(CSWATTN_ERR_INVALID_ARG, "k_pages and v_pages must differ");
+  if (q_out == q || q_out == k || q_out == v || q_out == ve)
+    return fail(CSWATTN_ERR_INVALID_ARG, "q_out must not alias an input");
+  ap.has_ve = layer->has_ve;
+  ap.eps = layer->eps;
+  ap.q = static_cast<const __nv_bfloat16*>(q);
+  ap.k = static_cast<const __nv_bfloat16*>(k);
+  ap.val = static_cast<const __nv_bfloat16*>(v);
+  ap.ve = static_cast<const __nv_bfloat16*>(ve);
+  ap.gate = static_cast<const __nv_bfloat16*>(gate);
+  ap.positions = positions;
+  ap.q_out = static_cast<__nv_bfloat16*>(q_out);
+  ap.k_pages = static_cast<__nv_bfloat16*>(k_pages);
+  ap.v_pages = static_cast<__nv_bfloat16*>(v_pages);
+  ap.weight = weight;
+  ap.position = position;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  const dim3 grid((paged->n_tokens + paged::kAppendTok - 1) / paged::kAppendTok);
+  {
+    ScopedTiming tm(CSWATTN_K_PROLOGUE, cs);
+    if (s.D == 64)
+      launch_pdl(interleaved ? paged::append_kernel<64, true> : paged::append_kernel<64, false>, grid,
+                 dim3(paged::kAppendThreads), 0, cs, ap);
+    else
+      launch_pdl(interleaved ? paged::append_kernel<128, true> : paged::append_kernel<128, false>, grid,
+                 dim3(paged::kAppendThreads), 0, cs, ap);
+  }
+  return launched("paged append launch");
+}
+
+size_t attn_paged_workspace_bytes(const cswattn_layer* layer, const cswattn_paged* paged) {
+  Shape s;
+  paged::View v;
+  if (check_paged(layer, paged, true, &s, &v) != CSWATTN_OK) return 0;
+  return 256;
+}
+
+cswattn_status attn_paged(const cswattn_layer* layer, const cswattn_paged* paged, const void* q_out,
+                          const void* k_pages, const void* v_pages, void* O, float* lse, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  const NvtxRange nvtx_range("attn_paged");
+  Shape s;
+  paged::AttendParams ap;
+  cswattn_status st = check_paged(layer, paged, true, &s, &ap.v);
+  if (st != CSWATTN_OK) return st;
+  if (paged->n_tokens == 0) return CSWATTN_OK;
+  CHECK_PTR(q_out, 16);
+  CHECK_PTR(k_pages, 16);
+  CHECK_PTR(v_pages, 16);
+  CHECK_PTR(O, 16);
+  CHECK_PTR(lse, 4);
+  CHECK_PTR(workspace, 256);
+  if (O == q_out) return fail(CSWATTN_ERR_INVALID_ARG, "O must not alias q_out");
+  const size_t need = attn_paged_workspace_bytes(layer, paged);
+  if (workspace_bytes < need)
+    return fail(CSWATTN_ERR_INVALID_ARG, "paged workspace too small: %zu < %zu bytes", workspace_bytes, need);
+  ap.scale = s.scale;
+  ap.q = static_cast<const __nv_bfloat16*>(q_out);
+  ap.k_pages = static_cast<const __nv_bfloat16*>(k_pages);
+  ap.v_pages = static_cast<const __nv_bfloat16*>(v_pages);
+  ap.O = static_cast<__nv_bfloat16*>(O);
+  ap.lse = lse;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  {
+    ScopedTiming tm(CSWATTN_K_DECODE, cs);
+    const dim3 grid(std::min<long long>(4096, (static_cast<long long>(ap.v.max_new) * s.H + 7) / 8), s.B);
+    launch_pdl(s.D == 64 ? paged::attend_simple_kernel<64> : paged::attend_simple_kernel<128>, grid, dim3(256), 0,
+               cs, ap);
+  }
+  return launched("paged attention launch");
+}
+
+cswattn_status attn_paged_weigh(const cswattn_layer* layer, const cswattn_paged* paged, const void* q_out,
+                                const void* k_pages, const float* lse, float* weight, void* stream) {
+  const NvtxRange nvtx_range("attn_paged_weigh");
+  Shape s;
+  paged::WeighParams wp;
+  cswattn_status st = check_paged(layer, paged, true, &s, &wp.v);
+  if (st != CSWATTN_OK) return st;
+  if (paged->n_tokens == 0) return CSWATTN_OK;
+  CHECK_PTR(q_out, 16);
+  CHECK_PTR(k_pages, 16);
+  CHECK_PTR(lse, 4);
+  CHECK_PTR(weight, 4);
+  wp.scale = s.scale;
+  wp.q = static_cast<const __nv_bfloat16*>(q_out);
+  wp.k_pages = static_cast<const __nv_bfloat16*>(k_pages);
+  wp.lse = lse;
+  wp.weight = weight;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  {
+    ScopedTiming tm(CSWATTN_K_DECODE, cs);
+    const dim3 grid(std::min<long long>(4096, (static_cast<long long>(s.T) * s.Hk + 7) / 8), s.B);
+    launch_pdl(s.D == 64 ? paged::weigh_simple_kernel<64> : paged::weigh_simple_kernel<128>, grid, dim3(256), 0, cs,
+               wp);
+  }
+  return launched("paged weights launch");
+}
+
+cswattn_status attn_paged_select(const cswattn_layer* layer, const cswattn_paged* paged, const float* weight,
+                                 const int* position, const int* next_pos, int n_keep, int n_recent, int* n_moves,
+                                 int* src, int* dst, int* new_len, void* stream) {
+  const NvtxRange nvtx_range("attn_paged_select");
+  Shape s;
+  paged::SelectParams sp;
+  cswattn_status st = check_paged(layer, paged, false, &s, &sp.v);
+  if (st != CSWATTN_OK) return st;
+  if (n_keep < 1 || n_keep > s.T)
+    return fail(CSWATTN_ERR_INVALID_ARG, "n_keep must be in [1, T = %d] (got %d)", s.T, n_keep);
+  if (n_recent < 0 || n_recent > n_keep)
+    return fail(CSWATTN_ERR_INVALID_ARG, "n_recent must be in [0, n_keep = %d] (got %d)", n_keep, n_recent);
+  CHECK_PTR(weight, 4);
+  CHECK_PTR(position, 4);
+  CHECK_PTR(next_pos, 4);
+  CHECK_PTR(n_moves, 4);
+  CHECK_PTR(src, 4);
+  CHECK_PTR(dst, 4);
+  CHECK_PTR(new_len, 4);
+  if (new_len == paged->cache_len) return fail(CSWATTN_ERR_INVALID_ARG, "new_len must not alias cache_len");
+  sp.weight = weight;
+  sp.position = position;
+  sp.next_pos = next_pos;
+  sp.n_keep = n_keep;
+  sp.n_recent = n_recent;
+  sp.smem_keys = std::min(s.T, paged::kSelectMaxKeys);
+  sp.n_moves = n_moves;
+  sp.src = src;
+  sp.dst = dst;
+  sp.new_len = new_len;
+  if ((st = set_smem(paged::select_kernel, paged::kSelectMaxKeys * 4)) != CSWATTN_OK) return st;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  {
+    ScopedTiming tm(CSWATTN_K_DECODE, cs);
+    launch_pdl(paged::select_kernel, dim3(s.Hk, s.B), dim3(paged::kSelectThreads),
+               static_cast<size_t>(sp.smem_keys) * 4, cs, sp);
+  }
+  return launched("paged select launch");
+}
+
+cswattn_status attn_paged_move(const cswattn_layer* layer, const cswattn_paged* paged, const int* n_moves,
+                               const int* src, const int* dst, int n_keep, void* k_pages, void* v_pages,
+                               float* weight, int* position, void* stream) {
+  const NvtxRange nvtx_range("attn_paged_move");
+  Shape s;
+  paged::MoveParams mp;
+  cswattn_status st = check_paged(layer, paged, false, &s, &mp.v);
+  if (st != CSWATTN_OK) return st;
+  if (n_keep < 1 || n_keep > s.T)
+    return fail(CSWATTN_ERR_INVALID_ARG, "n_keep must be in [1, T = %d] (got %d)", s.T, n_keep);
+  CHECK_PTR(n_moves, 4);
+  CHECK_PTR(src, 4);
+  CHECK_PTR(dst, 4);
+  CHECK_PTR(k_pages, 16);
+  CHECK_PTR(v_pages, 16);
+  CHECK_PTR(weight, 4);
+  CHECK_PTR(position, 4);
+  if (k_pages == v_pages) return fail(CSWATTN_ERR_INVALID_ARG, "k_pages and v_pages must differ");
+  mp.n_moves = n_moves;
+  mp.src = src;
+  mp.dst = dst;
+  mp.stride = n_keep;
+  mp.k_pages = static_cast<__nv_bfloat16*>(k_pages);
+  mp.v_pages = static_cast<__nv_bfloat16*>(v_pages);
+  mp.weight = weight;
+  mp.position = position;
+  // At most min(n_keep, T - n_keep) rows move per head.
+  const int most = std::min(n_keep, s.T - n_keep);
+  if (most == 0) return CSWATTN_OK;
+  const int per = paged::kMoveThreads / (s.D / 8);
+  const dim3 grid(std::min(1024, (most + per - 1) / per), s.Hk, s.B);
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  {
+    ScopedTiming tm(CSWATTN_K_DECODE, cs);
+    launch_pdl(s.D == 64 ? paged::move_kernel<64> : paged::move_kernel<128>, grid, dim3(paged::kMoveThreads), 0, cs,
+               mp);
+  }
+  return launched("paged move launch");
+}
+
+}  // extern "C"

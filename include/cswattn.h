@@ -300,6 +300,120 @@ cswattn_status attn_decode(const cswattn_layer* layer, const void* q, const void
                            void* k_cache, void* v_cache, void* O, float* lse, void* workspace,
                            size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------ paged cache
+ *
+ * Generation over a key/value cache whose rows lie in pages (the cache of
+ * page section "6. 추론 엔진 (nanochat/engine.py)", for many sequences of
+ * different lengths that share one pool of memory), with any number of new
+ * tokens per sequence in one call: a prompt's chunk, one generated token, or
+ * both side by side. Serving only: nothing here has a backward pass.
+ *
+ * layer: bf16, head_dim 64 or 128, n_head / n_kv_head <= 128. B is the number
+ * of sequences (at most 4096), T the most rows a sequence may reach
+ * (T <= pages_per_seq * page_size), window as in attn_fwd, counted in rows.
+ *
+ * A sequence b has cache_len[b] rows before the call and the new tokens
+ * new_start[b] .. new_start[b + 1] - 1; token i of it is row cache_len[b] + i,
+ * and it sees the rows (row - window, row]. Row r lies in page
+ * page_table[b][r / page_size], slot r % page_size. Table entries of rows that
+ * no new token sees are not read. Tokens at or past new_start[B] belong to
+ * nobody: their outputs are left as they were. No call changes cache_len.
+ *
+ * The lengths are device memory, which the host does not read. A sequence
+ * whose lengths do not fit (negative, decreasing new_start, tokens past
+ * n_tokens or max_new, rows past T) is left untouched, and so is a token or row
+ * whose page is not in [0, n_pages); the next cswattn_sync_status() returns
+ * CSWATTN_ERR_INVALID_ARG. (The attention of a sequence with such a page is
+ * computed as if its rows were zeros.) */
+typedef struct {
+  int page_size;         /* rows of a page, a multiple of 16 */
+  int n_pages;           /* pages of the pools */
+  int pages_per_seq;     /* columns of the page table */
+  int n_tokens;          /* rows of q, k, v, O, ... (new_start[B] or more) */
+  int max_new;           /* no sequence has more new tokens than this */
+  const int* page_table; /* device, (B, pages_per_seq) */
+  const int* cache_len;  /* device, (B) */
+  const int* new_start;  /* device, (B + 1), not decreasing */
+} cswattn_paged;
+
+/* Rotary positions of attn_paged_append. Pair i of the first rotary_dim
+ * elements of a head is rotated by position * frequencies[i]; the other
+ * elements pass through (normalised). A pair is (i, i + rotary_dim / 2), or
+ * (2i, 2i + 1) when interleaved. cos and sin are multiplied by `factor`. The
+ * angle is computed in float64. */
+typedef struct {
+  int rotary_dim;            /* multiple of 16, 16 .. head_dim */
+  int interleaved;           /* 0 or 1 */
+  float factor;              /* > 0; 1 unless the context is stretched with one */
+  const double* frequencies; /* host, rotary_dim / 2, or NULL: rope_base^(-2i/rotary_dim) */
+} cswattn_rope;
+
+/* The prologue (attn_prologue) of the new tokens, into the cache:
+ *   q_out = RoPE(RMSNorm(q))                       (n_tokens, n_head, head_dim)
+ *   k_pages[row of the token] = RoPE(RMSNorm(k))
+ *   v_pages[row of the token] = v + 3*sigmoid(gate)*ve  (v without has_ve)
+ *   weight[row] = 0, position[row] = the token's position, for each KV head.
+ * q (n_tokens, n_head, head_dim), k, v, ve (n_tokens, n_kv_head, head_dim),
+ * gate (n_tokens, n_kv_head). positions: device int32 (n_tokens), or NULL: a
+ * token's position is its row (they differ once rows have been evicted).
+ * rope NULL: the layer's plain RoPE. k_pages, v_pages (n_pages, page_size,
+ * n_kv_head, head_dim); weight (float32) and position (int32) (n_pages,
+ * n_kv_head, page_size), both or neither NULL. Every other row of the pools
+ * is left as it was. Two tokens must not share a row. */
+cswattn_status attn_paged_append(const cswattn_layer* layer, const cswattn_paged* paged,
+                                 const cswattn_rope* rope, const void* q, const void* k, const void* v,
+                                 const void* ve, const void* gate, const int* positions, void* q_out,
+                                 void* k_pages, void* v_pages, float* weight, int* position,
+                                 void* stream);
+
+/* Bytes of device scratch attn_paged needs; 0 for an invalid or unsupported
+ * layer or batch. Depends on the sizes alone, not on the device's lengths. */
+size_t attn_paged_workspace_bytes(const cswattn_layer* layer, const cswattn_paged* paged);
+
+/* Attention of the new tokens over the pages (attn_paged_append has written
+ * their rows): O (n_tokens, n_head, head_dim) and lse (n_tokens, n_head),
+ * natural log. workspace: at least attn_paged_workspace_bytes, 256-byte
+ * aligned; contents on entry do not matter; not to be used by another call in
+ * flight. */
+cswattn_status attn_paged(const cswattn_layer* layer, const cswattn_paged* paged, const void* q_out,
+                          const void* k_pages, const void* v_pages, void* O, float* lse,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
+/* Adds each visible row's attention weight to its accumulated one:
+ *   weight[row, kv head] += sum over the new tokens i that see the row and the
+ *   heads h of the group of exp(softmax_scale * q_out[i,h] . k[row] - lse[i,h])
+ * with attn_paged's lse. The sum's order is fixed: the same call on the same
+ * data gives the same bits. Pages must not be shared between sequences (each
+ * row of `weight` is updated without atomics). */
+cswattn_status attn_paged_weigh(const cswattn_layer* layer, const cswattn_paged* paged, const void* q_out,
+                                const void* k_pages, const float* lse, float* weight, void* stream);
+
+/* Which rows a sequence keeps when it may keep n_keep (1 .. T). For each
+ * sequence b and KV head, of its L = cache_len[b] rows: the rows with
+ * position >= next_pos[b] - n_recent come first (0 <= n_recent <= n_keep),
+ * then the others by larger weight (a NaN after all numbers); among the recent
+ * rows, and of equal weights, the lower row comes first. The first n_keep are
+ * kept. Kept rows at or past n_keep take the places of
+ * the evicted rows below n_keep, both in ascending order:
+ *   n_moves (B, n_kv_head), src, dst (B, n_kv_head, n_keep): row src[m] is to
+ *   be copied to row dst[m] for m < n_moves; entries from n_moves on are -1;
+ *   new_len (B) = min(L, n_keep), the sequence's rows after attn_paged_move.
+ * With L <= n_keep nothing moves. next_pos (B): the position of the next new
+ * token. new_len must not be cache_len itself. Of `paged`, page_size, n_pages,
+ * pages_per_seq, page_table and cache_len are used. */
+cswattn_status attn_paged_select(const cswattn_layer* layer, const cswattn_paged* paged, const float* weight,
+                                 const int* position, const int* next_pos, int n_keep, int n_recent,
+                                 int* n_moves, int* src, int* dst, int* new_len, void* stream);
+
+/* Copies K, V, weight and position of the moved rows (attn_paged_select's
+ * n_moves, src, dst with the same n_keep). Sources lie at or past n_keep,
+ * targets below it, so the copies are independent of one another. Attention
+ * afterwards takes new_len as the cache length; rows are no longer in the
+ * order of their positions, so the layer's window should cover all rows. */
+cswattn_status attn_paged_move(const cswattn_layer* layer, const cswattn_paged* paged, const int* n_moves,
+                               const int* src, const int* dst, int n_keep, void* k_pages, void* v_pages,
+                               float* weight, int* position, void* stream);
+
 /* bf16 matrix product on the tensor cores, the step Muon's orthogonalisation
  * is made of (page section "2. Muon 옵티마이저 (nanochat/optim.py)"):
  *   C[m][n] = alpha * sum_k Aop[m][k] * Bop[n][k] + beta * D[m][n]
@@ -341,7 +455,8 @@ cswattn_status muon_newton_schulz(int m, int n, const float* coeffs, int steps, 
  * the device status word of the
  * current device: CSWATTN_ERR_TIMEOUT if a kernel's bounded wait ran out
  * since the last check, CSWATTN_ERR_INVALID_ARG if a decode step met a cache
- * length outside [0, T), CSWATTN_ERR_BOUNDS if a bounds check of the
+ * length outside [0, T) or a paged call lengths, pages or moves that do not
+ * fit it, CSWATTN_ERR_BOUNDS if a bounds check of the
  * checked build (libcswattn_check.so, compiled with CSWATTN_CHECK=1) failed
  * (the access was skipped), CSWATTN_ERR_CUDA on a CUDA error, else
  * CSWATTN_OK. */
@@ -365,12 +480,13 @@ uint64_t cswattn_set_wait_limit_ns(uint64_t ns);
 
 /* Kernel kinds reported by cswattn_kernel_times(). */
 enum {
-  CSWATTN_K_PROLOGUE = 0, /* fused RMSNorm + RoPE + value residual */
+  CSWATTN_K_PROLOGUE = 0, /* fused RMSNorm + RoPE + value residual (into pages, too) */
   CSWATTN_K_FWD = 1,      /* attention forward (tensor cores, or fp32 CUDA cores) */
   CSWATTN_K_BWD_PRE = 2,  /* backward row terms Delta = rowsum(dO * O) */
   CSWATTN_K_BWD = 3,      /* attention backward main kernel(s) */
   CSWATTN_K_BWD_EPI = 4,  /* backward epilogue: RoPE^-1, RMSNorm', dv/dve/dgate */
-  CSWATTN_K_DECODE = 5,   /* decode step: new-token prologue, split-KV attention, combine */
+  CSWATTN_K_DECODE = 5,   /* decode step: new-token prologue, split-KV attention, combine;
+                             attention over pages, its row weights, eviction */
   CSWATTN_K_GATE_BWD = 6, /* backward of the value-embedding gate's projection */
   CSWATTN_K_GEMM = 7,     /* bf16 matrix product (the Newton-Schulz steps) */
   CSWATTN_NUM_KERNELS = 8
