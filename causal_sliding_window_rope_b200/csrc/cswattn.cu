@@ -28,6 +28,7 @@
 #include "fp8.cuh"
 #include "paged_append.cuh"
 #include "paged_simple.cuh"
+#include "paged_rows.cuh"
 #include "paged_evict.cuh"
 
 using namespace cswattn;

@@ -61,6 +61,61 @@ cswattn_status check_paged(const cswattn_layer* layer, const cswattn_paged* pg, 
   return CSWATTN_OK;
 }
 
+// Rows of a TMA box: the largest power of two that divides the page, at most
+// `most`; a block of rows is read as boxes that lie in one page each.
+int page_unit(int page_size, int most) {
+  int u = paged::kUnit;
+  while (u < most && page_size % (2 * u) == 0) u *= 2;
+  return u;
+}
+
+struct PagedWorkspace {
+  float* part_o;
+  float2* part_ml;
+  int2* info;
+  int slot_rows;  // query rows of a slot: 16, or 32 where a sequence may have more
+  size_t bytes;
+};
+
+PagedWorkspace carve_paged(const Shape& s, const paged::View& v, void* base) {
+  uint8_t* p = static_cast<uint8_t*>(base);
+  PagedWorkspace w;
+  w.slot_rows = static_cast<long long>(v.max_new) * s.g <= 16 ? 16 : 32;
+  const size_t rows = static_cast<size_t>(2 * paged::kSMs) * w.slot_rows;
+  size_t off = 0;
+  w.part_o = reinterpret_cast<float*>(p + off);
+  off += pad256(rows * s.D * 4);
+  w.part_ml = reinterpret_cast<float2*>(p + off);
+  off += pad256(rows * 8);
+  w.info = reinterpret_cast<int2*>(p + off);
+  off += pad256(static_cast<size_t>(s.B) * s.Hk * 8);
+  w.bytes = off;
+  return w;
+}
+
+// The kernel of few query rows and, behind it, the join of what it cut.
+template <int D, int MB>
+cswattn_status launch_rows_kernel(const paged::RowsParams& rp, const CUtensorMap& mk, const CUtensorMap& mv,
+                                  cudaStream_t st) {
+  using SM = paged::RowsSmem<D, MB>;
+  cswattn_status e = set_smem(paged::rows_kernel<D, MB>, SM::kBytes + 4 * (paged::kMaxSeqs + 1));
+  if (e != CSWATTN_OK) return e;
+  launch_pdl(paged::rows_kernel<D, MB>, dim3(paged::kSMs), dim3(32 * (paged::kKeyGroups * MB + 1)),
+             static_cast<size_t>(SM::kBytes) + 4 * (rp.v.B + 1), st, mk, mv, rp);
+  paged::CombineParams cp;
+  cp.v = rp.v;
+  cp.max_rows = 16 * MB;
+  cp.slot_rows = 16 * MB;
+  cp.part_o = rp.part_o;
+  cp.part_ml = rp.part_ml;
+  cp.info = rp.info;
+  cp.O = rp.O;
+  cp.lse = rp.lse;
+  launch_pdl(paged::combine_kernel<D>, dim3(static_cast<unsigned>(rp.v.B) * rp.v.Hk), dim3(paged::kCombineThreads), 0,
+             st, cp);
+  return CSWATTN_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -147,7 +202,7 @@ size_t attn_paged_workspace_bytes(const cswattn_layer* layer, const cswattn_page
   Shape s;
   paged::View v;
   if (check_paged(layer, paged, true, &s, &v) != CSWATTN_OK) return 0;
-  return 256;
+  return carve_paged(s, v, nullptr).bytes;
 }
 
 cswattn_status attn_paged(const cswattn_layer* layer, const cswattn_paged* paged, const void* q_out,
@@ -155,8 +210,8 @@ cswattn_status attn_paged(const cswattn_layer* layer, const cswattn_paged* paged
                           size_t workspace_bytes, void* stream) {
   const NvtxRange nvtx_range("attn_paged");
   Shape s;
-  paged::AttendParams ap;
-  cswattn_status st = check_paged(layer, paged, true, &s, &ap.v);
+  paged::View v;
+  cswattn_status st = check_paged(layer, paged, true, &s, &v);
   if (st != CSWATTN_OK) return st;
   if (paged->n_tokens == 0) return CSWATTN_OK;
   CHECK_PTR(q_out, 16);
@@ -166,18 +221,39 @@ cswattn_status attn_paged(const cswattn_layer* layer, const cswattn_paged* paged
   CHECK_PTR(lse, 4);
   CHECK_PTR(workspace, 256);
   if (O == q_out) return fail(CSWATTN_ERR_INVALID_ARG, "O must not alias q_out");
-  const size_t need = attn_paged_workspace_bytes(layer, paged);
-  if (workspace_bytes < need)
-    return fail(CSWATTN_ERR_INVALID_ARG, "paged workspace too small: %zu < %zu bytes", workspace_bytes, need);
-  ap.scale = s.scale;
-  ap.q = static_cast<const __nv_bfloat16*>(q_out);
-  ap.k_pages = static_cast<const __nv_bfloat16*>(k_pages);
-  ap.v_pages = static_cast<const __nv_bfloat16*>(v_pages);
-  ap.O = static_cast<__nv_bfloat16*>(O);
-  ap.lse = lse;
+  const PagedWorkspace w = carve_paged(s, v, workspace);
+  if (workspace_bytes < w.bytes)
+    return fail(CSWATTN_ERR_INVALID_ARG, "paged workspace too small: %zu < %zu bytes", workspace_bytes, w.bytes);
+  paged::RowsParams rp;
+  rp.v = v;
+  rp.scale_log2 = s.scale * 1.4426950408889634f;
+  rp.unit = page_unit(v.page_size, paged::kBlk);
+  rp.q = static_cast<const __nv_bfloat16*>(q_out);
+  rp.O = static_cast<__nv_bfloat16*>(O);
+  rp.lse = lse;
+  rp.part_o = w.part_o;
+  rp.part_ml = w.part_ml;
+  rp.info = w.info;
+  rp.wait_ns = g_wait_ns.load();
+  CUtensorMap mk, mv;
+  if ((st = make_map(&mk, k_pages, v.n_pages, v.page_size, s.Hk, rp.unit, s.D)) != CSWATTN_OK) return st;
+  if ((st = make_map(&mv, v_pages, v.n_pages, v.page_size, s.Hk, rp.unit, s.D)) != CSWATTN_OK) return st;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  {
-    ScopedTiming tm(CSWATTN_K_DECODE, cs);
+  ScopedTiming tm(CSWATTN_K_DECODE, cs);
+  const bool wide = w.slot_rows > 16;
+  st = s.D == 64 ? (wide ? launch_rows_kernel<64, 2>(rp, mk, mv, cs) : launch_rows_kernel<64, 1>(rp, mk, mv, cs))
+                 : (wide ? launch_rows_kernel<128, 2>(rp, mk, mv, cs) : launch_rows_kernel<128, 1>(rp, mk, mv, cs));
+  if (st != CSWATTN_OK) return st;
+  if (static_cast<long long>(v.max_new) * s.g > w.slot_rows) {
+    paged::AttendParams ap;
+    ap.v = v;
+    ap.scale = s.scale;
+    ap.min_rows = w.slot_rows + 1;
+    ap.q = rp.q;
+    ap.k_pages = static_cast<const __nv_bfloat16*>(k_pages);
+    ap.v_pages = static_cast<const __nv_bfloat16*>(v_pages);
+    ap.O = rp.O;
+    ap.lse = lse;
     const dim3 grid(std::min<long long>(4096, (static_cast<long long>(ap.v.max_new) * s.H + 7) / 8), s.B);
     launch_pdl(s.D == 64 ? paged::attend_simple_kernel<64> : paged::attend_simple_kernel<128>, grid, dim3(256), 0,
                cs, ap);

@@ -9,6 +9,7 @@ namespace paged {
 struct AttendParams {
   View v;
   float scale;
+  int min_rows;
   const __nv_bfloat16 *q, *k_pages, *v_pages;
   __nv_bfloat16* O;
   float* lse;
@@ -22,7 +23,7 @@ __global__ void __launch_bounds__(256) attend_simple_kernel(const AttendParams p
   const View& v = p.v;
   const int b = blockIdx.y, lane = lane_id();
   Seq s;
-  if (!seq_load(v, b, blockIdx.x == 0 && threadIdx.x == 0, s)) return;
+  if (!seq_load(v, b, blockIdx.x == 0 && threadIdx.x == 0, s) || s.n * v.g < p.min_rows) return;
   for (int w = blockIdx.x * 8 + warp_id(); w < s.n * v.H; w += gridDim.x * 8) {
     const int i = w / v.H, h = w % v.H, hk = h / v.g;
     const size_t row = static_cast<size_t>(s.tok0 + i) * v.H + h;
