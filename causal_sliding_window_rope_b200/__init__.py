@@ -13,6 +13,7 @@ value-embedding residual v + 3*sigmoid(gate)*ve.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from dataclasses import dataclass
@@ -306,6 +307,32 @@ def attn_decode(spec: LayerSpec, q, k, v, ve, gate, cache_len, k_cache, v_cache,
 
 # ------------------------------------------------------------------ paged cache
 
+@functools.lru_cache(maxsize=64)
+def _rope_frequencies(R, scaling, factor, base, original_length, beta_fast, beta_slow):
+    """(frequencies, factor on cos and sin) of RopeSpec's scalings."""
+    scale = 1.0
+    if scaling == "ntk":
+        if R == 2:
+            raise ValueError("ntk scaling needs rotary_dim > 2")
+        base = base * factor ** (R / (R - 2))
+    w = [base ** (-2.0 * i / R) for i in range(R // 2)]
+    if scaling == "linear":
+        w = [f / factor for f in w]
+    elif scaling == "yarn":
+        if not original_length or base == 1.0:
+            raise ValueError("yarn scaling needs original_length and a base other than 1")
+
+        def pair_of(turns):  # the pair that turns this often within original_length
+            return R * math.log(original_length / (turns * 2 * math.pi)) / (2 * math.log(base))
+        low = max(math.floor(pair_of(beta_fast)), 0)
+        high = min(math.ceil(pair_of(beta_slow)), R // 2 - 1)
+        for i in range(R // 2):
+            ramp = min(max((i - low) / max(high - low, 0.001), 0.0), 1.0)
+            w[i] = w[i] * (1 - ramp) + w[i] / factor * ramp
+        scale = 0.1 * math.log(factor) + 1.0
+    return tuple(w), scale, (ctypes.c_double * len(w))(*w)
+
+
 class RopeSpec:
     """Rotary positions of attn_paged_append: the layout (halves, or pairs of
     neighbours when interleaved), how much of the head turns, and the
@@ -334,35 +361,30 @@ class RopeSpec:
             raise ValueError(f"scaling must be one of {self.SCALINGS}, got {scaling!r}")
         if not (math.isfinite(factor) and factor > 0) or not (math.isfinite(base) and base > 0):
             raise ValueError("factor and base must be finite and > 0")
-        scale = 1.0
         if frequencies is not None:
-            w = [float(f) for f in frequencies]
+            w, scale = tuple(float(f) for f in frequencies), 1.0
             if len(w) != R // 2:
                 raise ValueError(f"{R // 2} frequencies are wanted, got {len(w)}")
+            array = (ctypes.c_double * len(w))(*w)
         else:
-            if scaling == "ntk":
-                if R == 2:
-                    raise ValueError("ntk scaling needs rotary_dim > 2")
-                base = base * factor ** (R / (R - 2))
-            w = [base ** (-2.0 * i / R) for i in range(R // 2)]
-            if scaling == "linear":
-                w = [f / factor for f in w]
-            elif scaling == "yarn":
-                if not original_length or base == 1.0:
-                    raise ValueError("yarn scaling needs original_length and a base other than 1")
-
-                def pair_of(turns):  # the pair that turns this often within original_length
-                    return R * math.log(original_length / (turns * 2 * math.pi)) / (2 * math.log(base))
-                low = max(math.floor(pair_of(beta_fast)), 0)
-                high = min(math.ceil(pair_of(beta_slow)), R // 2 - 1)
-                for i in range(R // 2):
-                    ramp = min(max((i - low) / max(high - low, 0.001), 0.0), 1.0)
-                    w[i] = w[i] * (1 - ramp) + w[i] / factor * ramp
-                scale = 0.1 * math.log(factor) + 1.0
-        self.rotary_dim, self.interleaved, self.frequencies = R, bool(interleaved), tuple(w)
+            w, scale, array = _rope_frequencies(R, scaling, factor, base, original_length, beta_fast, beta_slow)
+        self.rotary_dim, self.interleaved, self.frequencies = R, bool(interleaved), w
         self.attention_factor = float(scale if attention_factor is None else attention_factor)
-        self._freq = (ctypes.c_double * len(w))(*w)
-        self._c = CswattnRope(R, int(self.interleaved), self.attention_factor, self._freq)
+        self._c = CswattnRope(R, int(self.interleaved), self.attention_factor, array)
+
+
+def _want(device, *tensors):
+    """Each (name, tensor, shape, dtype): a contiguous CUDA tensor of that
+    shape and type on the device of this index."""
+    for name, t, shape, dtype in tensors:
+        if t is None:
+            raise ValueError(f"{name} is needed")
+        if t.dtype is not dtype or t.shape != shape:
+            raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+        if t.get_device() != device or device < 0:
+            raise ValueError(f"{name} must be a CUDA tensor on the device of the call's others, got {t.device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
 
 
 class PagedCache:
@@ -388,13 +410,24 @@ class PagedCache:
         else:
             raise ValueError("PagedCache needs n_pages and page_size, or the pools")
         kv, term = (n_pages, page_size, spec.n_kv_head, spec.head_dim), (n_pages, spec.n_kv_head, page_size)
-        for name, t, shape, dtype in (("k", k, kv, torch.bfloat16), ("v", v, kv, torch.bfloat16),
-                                      ("weight", weight, term, torch.float32),
-                                      ("position", position, term, torch.int32)):
-            if t is not None:
-                _want(name, t, shape, dtype)
+        self.device = (weight if k is None else k).get_device()
+        _want(self.device, *[x for x in (("k", k, kv, torch.bfloat16), ("v", v, kv, torch.bfloat16),
+                                         ("weight", weight, term, torch.float32),
+                                         ("position", position, term, torch.int32)) if x[1] is not None])
         self.k, self.v, self.weight, self.position = k, v, weight, position
-        self.n_pages, self.page_size = n_pages, page_size
+        self.n_pages, self.page_size, self.heads = n_pages, page_size, kv[2:]
+
+    def need(self, spec: LayerSpec, device, *names):
+        """The addresses of the pools of these names, for a call of `spec` on `device`."""
+        if self.heads != (spec.n_kv_head, spec.head_dim):
+            raise ValueError(f"the cache holds (n_kv_head, head_dim) = {self.heads}, the layer "
+                             f"{(spec.n_kv_head, spec.head_dim)}")
+        if self.device != device:
+            raise ValueError(f"the cache lies on cuda:{self.device}, the batch on cuda:{device}")
+        pools = [getattr(self, name) for name in names]
+        if any(t is None for t in pools):
+            raise ValueError(f"the cache has no {names[[t is None for t in pools].index(True)]}")
+        return [t.data_ptr() for t in pools]
 
 
 class PagedBatch:
@@ -406,10 +439,10 @@ class PagedBatch:
     def __init__(self, page_table, cache_len, new_start=None, n_tokens=0, max_new=0):
         import torch
         B, pages = page_table.shape
-        _want("page_table", page_table, (B, pages), torch.int32)
-        _want("cache_len", cache_len, (B,), torch.int32)
+        self.device = page_table.get_device()
+        _want(self.device, ("page_table", page_table, (B, pages), torch.int32), ("cache_len", cache_len, (B,), torch.int32))
         if new_start is not None:
-            _want("new_start", new_start, (B + 1,), torch.int32)
+            _want(self.device, ("new_start", new_start, (B + 1,), torch.int32))
         self.page_table, self.cache_len, self.new_start = page_table, cache_len, new_start
         self.n_tokens, self.max_new = int(n_tokens), int(max_new)
 
@@ -422,27 +455,25 @@ class PagedBatch:
                             None if self.new_start is None else self.new_start.data_ptr())
 
 
-def _want(name, t, shape, dtype):
-    if t is None:
-        raise ValueError(f"{name} is needed")
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-
-
-def _same_device(batch: PagedBatch, *tensors):
-    """All tensors of a paged call lie on the page table's device; the call
-    is made with that device current (its context is the one the kernels are
-    launched in)."""
+def _paged_call(fn, device, stream, *args):
+    """Calls an entry point with the tensors' device current (the kernels run
+    in its context) on the stream given, or on that device's current one."""
     import torch
-    device = batch.page_table.device
-    for t in (batch.cache_len, batch.new_start, *tensors):
-        if t is not None and t.device != device:
-            raise ValueError(f"tensors of a paged call lie on {device} and {t.device}")
-    return torch.cuda.device(device)
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(device)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if torch._C._cuda_getDevice() == device:
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, stream)
+    if status != OK:
+        _check(status)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def attn_paged_append(spec: LayerSpec, batch: PagedBatch, cache: PagedCache, q, k, v, ve, gate, q_out,
@@ -450,27 +481,22 @@ def attn_paged_append(spec: LayerSpec, batch: PagedBatch, cache: PagedCache, q, 
     """The prologue of the batch's new tokens: q_out, and their rows of the
     cache. rope None: the layer's plain RoPE."""
     import torch
-    N, H, Hk, D = batch.n_tokens, spec.n_head, spec.n_kv_head, spec.head_dim
-    bf = torch.bfloat16
-    for name, t, shape in (("q", q, (N, H, D)), ("k", k, (N, Hk, D)), ("v", v, (N, Hk, D)), ("q_out", q_out, (N, H, D))):
-        _want(name, t, shape, bf)
+    N, H, Hk, D, dev = batch.n_tokens, spec.n_head, spec.n_kv_head, spec.head_dim, batch.device
+    bf, qs, ks = torch.bfloat16, (N, H, D), (N, Hk, D)
+    _want(dev, ("q", q, qs, bf), ("k", k, ks, bf), ("v", v, ks, bf), ("q_out", q_out, qs, bf))
     if spec.has_ve:
-        _want("ve", ve, (N, Hk, D), bf)
-        _want("gate", gate, (N, Hk), bf)
+        _want(dev, ("ve", ve, ks, bf), ("gate", gate, (N, Hk), bf))
     if positions is not None:
-        _want("positions", positions, (N,), torch.int32)
-    layer, paged = spec.c(), batch.c(spec, cache)
-    with _same_device(batch, q, k, v, ve, gate, q_out, positions, cache.k, cache.v, cache.weight, cache.position):
-        _check(lib().attn_paged_append(ctypes.byref(layer), ctypes.byref(paged),
-                                       None if rope is None else ctypes.byref(rope._c), _ptr(q), _ptr(k), _ptr(v),
-                                       _ptr(ve), _ptr(gate), _ptr(positions), _ptr(q_out), _ptr(cache.k),
-                                       _ptr(cache.v), _ptr(cache.weight), _ptr(cache.position), _stream(stream)))
+        _want(dev, ("positions", positions, (N,), torch.int32))
+    _paged_call(lib().attn_paged_append, dev, stream, ctypes.byref(spec.c()), ctypes.byref(batch.c(spec, cache)),
+                None if rope is None else ctypes.byref(rope._c), q.data_ptr(), k.data_ptr(), v.data_ptr(), _at(ve),
+                _at(gate), _at(positions), q_out.data_ptr(), *cache.need(spec, dev, "k", "v"), _at(cache.weight),
+                _at(cache.position))
 
 
 def attn_paged_workspace_bytes(spec: LayerSpec, batch: PagedBatch, cache: PagedCache) -> int:
     """Scratch bytes of attn_paged for this layer and the batch's sizes."""
-    layer, paged = spec.c(), batch.c(spec, cache)
-    return int(lib().attn_paged_workspace_bytes(ctypes.byref(layer), ctypes.byref(paged)))
+    return int(lib().attn_paged_workspace_bytes(ctypes.byref(spec.c()), ctypes.byref(batch.c(spec, cache))))
 
 
 def attn_paged(spec: LayerSpec, batch: PagedBatch, cache: PagedCache, q_out, O, lse, workspace,
@@ -478,28 +504,25 @@ def attn_paged(spec: LayerSpec, batch: PagedBatch, cache: PagedCache, q_out, O, 
     """Attention of the new tokens (q_out of attn_paged_append) over the
     cache: O (n_tokens, H, D) and lse (n_tokens, H)."""
     import torch
-    N, H, D = batch.n_tokens, spec.n_head, spec.head_dim
-    _want("q_out", q_out, (N, H, D), torch.bfloat16)
-    _want("O", O, (N, H, D), torch.bfloat16)
-    _want("lse", lse, (N, H), torch.float32)
-    layer, paged = spec.c(), batch.c(spec, cache)
+    N, H, D, dev = batch.n_tokens, spec.n_head, spec.head_dim, batch.device
+    bf, qs = torch.bfloat16, (N, H, D)
+    _want(dev, ("q_out", q_out, qs, bf), ("O", O, qs, bf), ("lse", lse, (N, H), torch.float32),
+          ("workspace", workspace, workspace.shape, workspace.dtype))
     if workspace_bytes is None:
         workspace_bytes = workspace.numel() * workspace.element_size()
-    with _same_device(batch, q_out, O, lse, workspace, cache.k, cache.v):
-        _check(lib().attn_paged(ctypes.byref(layer), ctypes.byref(paged), _ptr(q_out), _ptr(cache.k), _ptr(cache.v),
-                                _ptr(O), _ptr(lse), _ptr(workspace), workspace_bytes, _stream(stream)))
+    _paged_call(lib().attn_paged, dev, stream, ctypes.byref(spec.c()), ctypes.byref(batch.c(spec, cache)),
+                q_out.data_ptr(), *cache.need(spec, dev, "k", "v"), O.data_ptr(), lse.data_ptr(),
+                workspace.data_ptr(), workspace_bytes)
 
 
 def attn_paged_weigh(spec: LayerSpec, batch: PagedBatch, cache: PagedCache, q_out, lse, stream=None):
     """Adds the new tokens' attention weights to cache.weight."""
     import torch
-    N, H, D = batch.n_tokens, spec.n_head, spec.head_dim
-    _want("q_out", q_out, (N, H, D), torch.bfloat16)
-    _want("lse", lse, (N, H), torch.float32)
-    layer, paged = spec.c(), batch.c(spec, cache)
-    with _same_device(batch, q_out, lse, cache.k, cache.weight):
-        _check(lib().attn_paged_weigh(ctypes.byref(layer), ctypes.byref(paged), _ptr(q_out), _ptr(cache.k),
-                                      _ptr(lse), _ptr(cache.weight), _stream(stream)))
+    N, H, dev = batch.n_tokens, spec.n_head, batch.device
+    _want(dev, ("q_out", q_out, (N, H, spec.head_dim), torch.bfloat16), ("lse", lse, (N, H), torch.float32))
+    k, weight = cache.need(spec, dev, "k", "weight")
+    _paged_call(lib().attn_paged_weigh, dev, stream, ctypes.byref(spec.c()), ctypes.byref(batch.c(spec, cache)),
+                q_out.data_ptr(), k, lse.data_ptr(), weight)
 
 
 def attn_paged_select(spec: LayerSpec, batch: PagedBatch, cache: PagedCache, next_pos, n_keep, n_recent, n_moves,
@@ -507,30 +530,24 @@ def attn_paged_select(spec: LayerSpec, batch: PagedBatch, cache: PagedCache, nex
     """Which rows each KV head keeps under a budget of n_keep rows, as moves
     (src, dst) of n_moves rows, and the sequences' new lengths."""
     import torch
-    B, Hk = spec.B, spec.n_kv_head
-    i32 = torch.int32
-    for name, t, shape in (("next_pos", next_pos, (B,)), ("n_moves", n_moves, (B, Hk)), ("src", src, (B, Hk, n_keep)),
-                           ("dst", dst, (B, Hk, n_keep)), ("new_len", new_len, (B,))):
-        _want(name, t, shape, i32)
-    layer, paged = spec.c(), batch.c(spec, cache)
-    with _same_device(batch, next_pos, n_moves, src, dst, new_len, cache.weight, cache.position):
-        _check(lib().attn_paged_select(ctypes.byref(layer), ctypes.byref(paged), _ptr(cache.weight),
-                                       _ptr(cache.position), _ptr(next_pos), int(n_keep), int(n_recent),
-                                       _ptr(n_moves), _ptr(src), _ptr(dst), _ptr(new_len), _stream(stream)))
+    B, Hk, dev = spec.B, spec.n_kv_head, batch.device
+    i32, ms = torch.int32, (B, Hk, n_keep)
+    _want(dev, ("next_pos", next_pos, (B,), i32), ("n_moves", n_moves, (B, Hk), i32), ("src", src, ms, i32),
+          ("dst", dst, ms, i32), ("new_len", new_len, (B,), i32))
+    _paged_call(lib().attn_paged_select, dev, stream, ctypes.byref(spec.c()), ctypes.byref(batch.c(spec, cache)),
+                *cache.need(spec, dev, "weight", "position"), next_pos.data_ptr(), n_keep, n_recent,
+                n_moves.data_ptr(), src.data_ptr(), dst.data_ptr(), new_len.data_ptr())
 
 
 def attn_paged_move(spec: LayerSpec, batch: PagedBatch, cache: PagedCache, n_moves, src, dst, stream=None):
     """Moves the kept rows of attn_paged_select to their new places."""
     import torch
-    B, Hk, n_keep = src.shape
-    _want("n_moves", n_moves, (spec.B, spec.n_kv_head), torch.int32)
-    _want("src", src, (spec.B, spec.n_kv_head, n_keep), torch.int32)
-    _want("dst", dst, (spec.B, spec.n_kv_head, n_keep), torch.int32)
-    layer, paged = spec.c(), batch.c(spec, cache)
-    with _same_device(batch, n_moves, src, dst, cache.k, cache.v, cache.weight, cache.position):
-        _check(lib().attn_paged_move(ctypes.byref(layer), ctypes.byref(paged), _ptr(n_moves), _ptr(src), _ptr(dst),
-                                     int(n_keep), _ptr(cache.k), _ptr(cache.v), _ptr(cache.weight),
-                                     _ptr(cache.position), _stream(stream)))
+    B, Hk, n_keep, dev = spec.B, spec.n_kv_head, src.shape[-1], batch.device
+    i32, ms = torch.int32, (B, Hk, n_keep)
+    _want(dev, ("n_moves", n_moves, (B, Hk), i32), ("src", src, ms, i32), ("dst", dst, ms, i32))
+    _paged_call(lib().attn_paged_move, dev, stream, ctypes.byref(spec.c()), ctypes.byref(batch.c(spec, cache)),
+                n_moves.data_ptr(), src.data_ptr(), dst.data_ptr(), n_keep,
+                *cache.need(spec, dev, "k", "v", "weight", "position"))
 
 
 def cswattn_sync_status(stream=None):

@@ -29,6 +29,7 @@
 #include "paged_append.cuh"
 #include "paged_simple.cuh"
 #include "paged_rows.cuh"
+#include "paged_tile.cuh"
 #include "paged_evict.cuh"
 
 using namespace cswattn;

@@ -74,6 +74,11 @@ struct PagedWorkspace {
   float2* part_ml;
   int2* info;
   int slot_rows;  // query rows of a slot: 16, or 32 where a sequence may have more
+  bool tiles;     // a sequence may have more query rows than that
+  paged::Plan* plan;
+  int* longs;
+  float* tile_o;
+  float2* tile_ml;
   size_t bytes;
 };
 
@@ -89,8 +94,53 @@ PagedWorkspace carve_paged(const Shape& s, const paged::View& v, void* base) {
   off += pad256(rows * 8);
   w.info = reinterpret_cast<int2*>(p + off);
   off += pad256(static_cast<size_t>(s.B) * s.Hk * 8);
+  w.tiles = static_cast<long long>(v.max_new) * s.g > w.slot_rows;
+  w.plan = nullptr;
+  w.longs = nullptr;
+  w.tile_o = nullptr;
+  w.tile_ml = nullptr;
+  if (w.tiles) {
+    const size_t tile_rows = static_cast<size_t>(2 * paged::kSMs) * 256;
+    w.plan = reinterpret_cast<paged::Plan*>(p + off);
+    off += pad256(sizeof(paged::Plan));
+    w.longs = reinterpret_cast<int*>(p + off);
+    off += pad256(static_cast<size_t>(s.B) * 4);
+    w.tile_o = reinterpret_cast<float*>(p + off);
+    off += pad256(tile_rows * s.D * 4);
+    w.tile_ml = reinterpret_cast<float2*>(p + off);
+    off += pad256(tile_rows * 8);
+  }
   w.bytes = off;
   return w;
+}
+
+// Tensor map of q (n_tokens, H, D) whose box is one 64-column panel of `tpt`
+// tokens x g heads: the 128 rows (or fewer) of a tile, tokens outermost.
+cswattn_status make_map_group(CUtensorMap* map, const void* base, int n_tokens, int H, int D, int g, int tpt) {
+  EncodeTiledFn enc;
+  cswattn_status s = get_encoder(&enc);
+  if (s != CSWATTN_OK) return s;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(H),
+                              static_cast<cuuint64_t>(n_tokens)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(H) * D * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(g), static_cast<cuuint32_t>(tpt)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(CSWATTN_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+  return CSWATTN_OK;
+}
+
+// The kernels of many query rows: the deal, the tiles, the join of what was cut.
+template <int D>
+void launch_tile_kernels(const paged::TileParams& tp, paged::Plan* plan, int* longs, const CUtensorMap& mq,
+                         const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t st) {
+  launch_pdl(paged::plan_kernel, dim3(1), dim3(paged::kPlanThreads), 0, st, tp.v, tp.tpt, tp.short_rows, plan, longs);
+  launch_pdl(paged::tile_kernel<D>, dim3(paged::kSMs), dim3(paged::kTileThreads), paged::TileSmem<D>::kBytes, st, mq,
+             mk, mv, tp);
+  launch_pdl(paged::tile_combine_kernel<D>, dim3(paged::kSMs - 1, 256 / paged::kTileCombineRows),
+             dim3(32 * paged::kTileCombineRows), 0, st, tp);
 }
 
 // The kernel of few query rows and, behind it, the join of what it cut.
@@ -238,26 +288,38 @@ cswattn_status attn_paged(const cswattn_layer* layer, const cswattn_paged* paged
   CUtensorMap mk, mv;
   if ((st = make_map(&mk, k_pages, v.n_pages, v.page_size, s.Hk, rp.unit, s.D)) != CSWATTN_OK) return st;
   if ((st = make_map(&mv, v_pages, v.n_pages, v.page_size, s.Hk, rp.unit, s.D)) != CSWATTN_OK) return st;
+  // What may fail is done before anything is enqueued.
+  CUtensorMap mq, mk128, mv128;
+  paged::TileParams tp;
+  if (w.tiles) {
+    tp.v = v;
+    tp.scale_log2 = rp.scale_log2;
+    tp.unit = page_unit(v.page_size, 128);
+    tp.tpt = 128 / s.g;
+    tp.short_rows = w.slot_rows;
+    tp.plan = w.plan;
+    tp.longs = w.longs;
+    tp.O = rp.O;
+    tp.lse = lse;
+    tp.part_o = w.tile_o;
+    tp.part_ml = w.tile_ml;
+    tp.wait_ns = rp.wait_ns;
+    if ((st = make_map_group(&mq, q_out, v.n_tokens, s.H, s.D, s.g, tp.tpt)) != CSWATTN_OK) return st;
+    if ((st = make_map(&mk128, k_pages, v.n_pages, v.page_size, s.Hk, tp.unit, s.D)) != CSWATTN_OK) return st;
+    if ((st = make_map(&mv128, v_pages, v.n_pages, v.page_size, s.Hk, tp.unit, s.D)) != CSWATTN_OK) return st;
+    st = s.D == 64 ? set_smem(paged::tile_kernel<64>, paged::TileSmem<64>::kBytes)
+                   : set_smem(paged::tile_kernel<128>, paged::TileSmem<128>::kBytes);
+    if (st != CSWATTN_OK) return st;
+  }
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   ScopedTiming tm(CSWATTN_K_DECODE, cs);
   const bool wide = w.slot_rows > 16;
   st = s.D == 64 ? (wide ? launch_rows_kernel<64, 2>(rp, mk, mv, cs) : launch_rows_kernel<64, 1>(rp, mk, mv, cs))
                  : (wide ? launch_rows_kernel<128, 2>(rp, mk, mv, cs) : launch_rows_kernel<128, 1>(rp, mk, mv, cs));
   if (st != CSWATTN_OK) return st;
-  if (static_cast<long long>(v.max_new) * s.g > w.slot_rows) {
-    paged::AttendParams ap;
-    ap.v = v;
-    ap.scale = s.scale;
-    ap.min_rows = w.slot_rows + 1;
-    ap.q = rp.q;
-    ap.k_pages = static_cast<const __nv_bfloat16*>(k_pages);
-    ap.v_pages = static_cast<const __nv_bfloat16*>(v_pages);
-    ap.O = rp.O;
-    ap.lse = lse;
-    const dim3 grid(std::min<long long>(4096, (static_cast<long long>(ap.v.max_new) * s.H + 7) / 8), s.B);
-    launch_pdl(s.D == 64 ? paged::attend_simple_kernel<64> : paged::attend_simple_kernel<128>, grid, dim3(256), 0,
-               cs, ap);
-  }
+  if (w.tiles)
+    s.D == 64 ? launch_tile_kernels<64>(tp, w.plan, w.longs, mq, mk128, mv128, cs)
+              : launch_tile_kernels<128>(tp, w.plan, w.longs, mq, mk128, mv128, cs);
   return launched("paged attention launch");
 }
 
