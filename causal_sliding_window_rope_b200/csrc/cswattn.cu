@@ -27,9 +27,9 @@
 #include "qkv_sm100.cuh"
 #include "fp8.cuh"
 #include "paged_append.cuh"
-#include "paged_simple.cuh"
 #include "paged_rows.cuh"
 #include "paged_tile.cuh"
+#include "paged_weigh.cuh"
 #include "paged_evict.cuh"
 
 using namespace cswattn;

@@ -166,6 +166,22 @@ cswattn_status launch_rows_kernel(const paged::RowsParams& rp, const CUtensorMap
   return CSWATTN_OK;
 }
 
+template <int D, int NT>
+cswattn_status launch_weigh_rows_nt(const paged::WeighRowsParams& rp, const CUtensorMap& mk, cudaStream_t st) {
+  using SM = paged::WeighRowsSmem<D>;
+  cswattn_status e = set_smem(paged::weigh_rows_kernel<D, NT>, SM::kBytes + 4 * (paged::kMaxSeqs + 1));
+  if (e != CSWATTN_OK) return e;
+  launch_pdl(paged::weigh_rows_kernel<D, NT>, dim3(paged::kSMs), dim3(32 * (4 * paged::kWeighGroups + 1)),
+             static_cast<size_t>(SM::kBytes) + 4 * (rp.v.B + 1), st, mk, rp);
+  return CSWATTN_OK;
+}
+template <int D>
+cswattn_status launch_weigh_rows(const paged::WeighRowsParams& rp, const CUtensorMap& mk, cudaStream_t st) {
+  return rp.max_rows == 8    ? launch_weigh_rows_nt<D, 1>(rp, mk, st)
+         : rp.max_rows == 16 ? launch_weigh_rows_nt<D, 2>(rp, mk, st)
+                             : launch_weigh_rows_nt<D, 4>(rp, mk, st);
+}
+
 }  // namespace
 
 extern "C" {
@@ -327,25 +343,56 @@ cswattn_status attn_paged_weigh(const cswattn_layer* layer, const cswattn_paged*
                                 const void* k_pages, const float* lse, float* weight, void* stream) {
   const NvtxRange nvtx_range("attn_paged_weigh");
   Shape s;
-  paged::WeighParams wp;
-  cswattn_status st = check_paged(layer, paged, true, &s, &wp.v);
+  paged::View v;
+  cswattn_status st = check_paged(layer, paged, true, &s, &v);
   if (st != CSWATTN_OK) return st;
   if (paged->n_tokens == 0) return CSWATTN_OK;
   CHECK_PTR(q_out, 16);
   CHECK_PTR(k_pages, 16);
   CHECK_PTR(lse, 4);
   CHECK_PTR(weight, 4);
-  wp.scale = s.scale;
-  wp.q = static_cast<const __nv_bfloat16*>(q_out);
-  wp.k_pages = static_cast<const __nv_bfloat16*>(k_pages);
-  wp.lse = lse;
-  wp.weight = weight;
+  const long long rows = static_cast<long long>(v.max_new) * s.g;
+  paged::WeighRowsParams rp;
+  rp.v = v;
+  rp.scale_log2 = s.scale * 1.4426950408889634f;
+  rp.unit = page_unit(v.page_size, paged::kBlk);
+  rp.max_rows = rows <= 8 ? 8 : (rows <= 16 ? 16 : 32);
+  rp.q = static_cast<const __nv_bfloat16*>(q_out);
+  rp.lse = lse;
+  rp.weight = weight;
+  rp.wait_ns = g_wait_ns.load();
+  paged::WeighTileParams tp;
+  CUtensorMap mk, mq, mk128;
+  if ((st = make_map(&mk, k_pages, v.n_pages, v.page_size, s.Hk, rp.unit, s.D)) != CSWATTN_OK) return st;
+  const bool tiles = rows > rp.max_rows;
+  if (tiles) {
+    tp.v = v;
+    tp.scale_log2 = rp.scale_log2;
+    tp.unit = page_unit(v.page_size, 128);
+    tp.tpt = 128 / s.g;
+    tp.short_rows = rp.max_rows;
+    tp.lse = lse;
+    tp.weight = weight;
+    tp.wait_ns = rp.wait_ns;
+    if ((st = make_map_group(&mq, q_out, v.n_tokens, s.H, s.D, s.g, tp.tpt)) != CSWATTN_OK) return st;
+    if ((st = make_map(&mk128, k_pages, v.n_pages, v.page_size, s.Hk, tp.unit, s.D)) != CSWATTN_OK) return st;
+    const int extra = 4 * (paged::kMaxSeqs + 1);
+    st = s.D == 64 ? set_smem(paged::weigh_tile_kernel<64>, paged::WeighTileSmem<64>::kBytes + extra)
+                   : set_smem(paged::weigh_tile_kernel<128>, paged::WeighTileSmem<128>::kBytes + extra);
+    if (st != CSWATTN_OK) return st;
+  }
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  {
-    ScopedTiming tm(CSWATTN_K_DECODE, cs);
-    const dim3 grid(std::min<long long>(4096, (static_cast<long long>(s.T) * s.Hk + 7) / 8), s.B);
-    launch_pdl(s.D == 64 ? paged::weigh_simple_kernel<64> : paged::weigh_simple_kernel<128>, grid, dim3(256), 0, cs,
-               wp);
+  ScopedTiming tm(CSWATTN_K_DECODE, cs);
+  st = s.D == 64 ? launch_weigh_rows<64>(rp, mk, cs) : launch_weigh_rows<128>(rp, mk, cs);
+  if (st != CSWATTN_OK) return st;
+  if (tiles) {
+    const dim3 grid(paged::kWeighCtas), block(paged::kWeighThreads);
+    const size_t pre = static_cast<size_t>(4) * (v.B + 1);
+    if (s.D == 64)
+      launch_pdl(paged::weigh_tile_kernel<64>, grid, block, paged::WeighTileSmem<64>::kBytes + pre, cs, mq, mk128, tp);
+    else
+      launch_pdl(paged::weigh_tile_kernel<128>, grid, block, paged::WeighTileSmem<128>::kBytes + pre, cs, mq, mk128,
+                 tp);
   }
   return launched("paged weights launch");
 }
