@@ -422,7 +422,12 @@ cswattn_status attn_paged_select(const cswattn_layer* layer, const cswattn_paged
   sp.next_pos = next_pos;
   sp.n_keep = n_keep;
   sp.n_recent = n_recent;
-  sp.smem_keys = std::min(s.T, paged::kSelectMaxKeys);
+  // CTAs per head: enough rows for each, and no more CTAs than the SMs hold at once.
+  int ranks = 1;
+  while (ranks < paged::kSelectMaxCluster && s.T > ranks * paged::kSelectRows &&
+         2ll * ranks * s.B * s.Hk <= paged::kSMs)
+    ranks *= 2;
+  sp.smem_keys = std::min((s.T + ranks - 1) / ranks, paged::kSelectMaxKeys);
   sp.n_moves = n_moves;
   sp.src = src;
   sp.dst = dst;
@@ -431,8 +436,8 @@ cswattn_status attn_paged_select(const cswattn_layer* layer, const cswattn_paged
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   {
     ScopedTiming tm(CSWATTN_K_DECODE, cs);
-    launch_pdl(paged::select_kernel, dim3(s.Hk, s.B), dim3(paged::kSelectThreads),
-               static_cast<size_t>(sp.smem_keys) * 4, cs, sp);
+    launch_pdl_cluster(paged::select_kernel, dim3(ranks, s.Hk, s.B), dim3(paged::kSelectThreads),
+                       static_cast<size_t>(sp.smem_keys) * 4, static_cast<unsigned>(ranks), cs, sp);
   }
   return launched("paged select launch");
 }
@@ -466,8 +471,9 @@ cswattn_status attn_paged_move(const cswattn_layer* layer, const cswattn_paged* 
   // At most min(n_keep, T - n_keep) rows move per head.
   const int most = std::min(n_keep, s.T - n_keep);
   if (most == 0) return CSWATTN_OK;
-  const int per = paged::kMoveThreads / (s.D / 8);
-  const dim3 grid(std::min(1024, (most + per - 1) / per), s.Hk, s.B);
+  const int per = paged::kMoveThreads / (s.D / 8) * paged::kMoveBatch;
+  const int share = std::max(1, paged::kMoveCtas / (s.B * s.Hk));
+  const dim3 grid(std::min(share, (most + per - 1) / per), s.Hk, s.B);
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   {
     ScopedTiming tm(CSWATTN_K_DECODE, cs);

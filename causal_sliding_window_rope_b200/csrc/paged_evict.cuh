@@ -10,13 +10,16 @@
 // position, and attention over rows that are all visible does not depend on
 // their order.
 #pragma once
-#include "paged.cuh"
+#include "paged_weigh.cuh"
 
 namespace cswattn {
 namespace paged {
 
 constexpr int kSelectThreads = 1024;
-constexpr int kSelectMaxKeys = 48 << 10;  // keys held in shared memory; further rows are read again
+constexpr int kSelectMaxKeys = 48 << 10;   // keys a CTA holds in shared memory; further rows are read again
+constexpr int kSelectMaxCluster = 8;       // CTAs that share one head's rows
+constexpr int kSelectRows = 2048;          // rows worth a CTA of their own
+constexpr int kBins = 2048;                // bins of one radix pass
 
 struct SelectParams {
   View v;
@@ -35,114 +38,175 @@ __device__ __forceinline__ uint32_t weight_order(float w) {
   return (u >> 31) ? ~u : (u | 0x80000000u);
 }
 
+// Shared memory of the cluster's CTA `rank` at the place of p.
+__device__ __forceinline__ uint32_t peer_load(const void* p, int rank) {
+  uint32_t a, y;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(y) : "r"(a) : "memory");
+  return y;
+}
+
+// A cluster of gridDim.x CTAs = (sequence, KV head), each with a run of
+// consecutive rows. The n_keep-th largest key comes from three radix passes
+// (11, 11, 10 bits): each CTA counts its rows' digits, the counts of all
+// CTAs are read through the cluster's shared memory. Bound by latency, so the
+// rows are read once (keys stay in shared memory) and long heads are spread
+// over up to 8 SMs. Every path of a cluster's CTAs meets the same barriers.
 __global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectParams p) {
   extern __shared__ uint32_t s_key[];
-  __shared__ uint32_t s_hist[2048];
-  __shared__ int s_warp[3][32];
+  __shared__ uint32_t s_hist[2][kBins];  // two, so that a pass needs one meeting of the cluster
+  __shared__ uint32_t s_warp[32];
   __shared__ uint32_t s_pick[2];
+  __shared__ uint32_t s_count[3];        // this CTA's ties, holes, movers
   const View& v = p.v;
-  const int hk = blockIdx.x, b = blockIdx.y;
-  const int warp = warp_id(), lane = lane_id();
+  const int rank = blockIdx.x, ranks = gridDim.x, hk = blockIdx.y, b = blockIdx.z;
+  const int warp = warp_id(), lane = lane_id(), tid = threadIdx.x;
   pdl_launch_dependents();
+  for (int i = tid; i < 2 * kBins; i += kSelectThreads) (&s_hist[0][0])[i] = 0u;
   pdl_wait();
   const int L = v.cache_len[b];
   const size_t head = static_cast<size_t>(b) * v.Hk + hk;
+  const bool lead = rank == 0;
   if (L < 0 || L > v.T) {
-    if (hk == 0 && threadIdx.x == 0) atomicOr(&g_status, kStatusRange);
+    if (lead && hk == 0 && tid == 0) atomicOr(&g_status, kStatusRange);
     return;
   }
-  if (hk == 0 && threadIdx.x == 0) p.new_len[b] = min(L, p.n_keep);
+  if (lead && hk == 0 && tid == 0) p.new_len[b] = min(L, p.n_keep);
   int* src = p.src + head * p.n_keep;
   int* dst = p.dst + head * p.n_keep;
   if (L <= p.n_keep) {
-    if (threadIdx.x == 0) p.n_moves[head] = 0;
-    for (int i = threadIdx.x; i < p.n_keep; i += kSelectThreads) src[i] = dst[i] = -1;
+    if (lead && tid == 0) p.n_moves[head] = 0;
+    for (int i = rank * kSelectThreads + tid; i < p.n_keep; i += ranks * kSelectThreads) src[i] = dst[i] = -1;
     return;
   }
+  // This CTA's rows [base, base + mine).
+  const int per = (L + ranks - 1) / ranks;
+  const int base = min(L, rank * per), mine = min(L - base, per);
   // 64 bits: next_pos - n_recent may pass the smallest int
   const long long recent = static_cast<long long>(p.next_pos[b]) - p.n_recent;
-  auto compute = [&](int r) -> uint32_t {
+  auto compute = [&](int i) -> uint32_t {
+    const int r = base + i;
     const int page = page_at(v, b, r / v.page_size);
     if (page < 0) return 0u;
     const size_t at = term_index(v, page, r % v.page_size, hk);
-    return p.position[at] >= recent ? 0xFFFFFFFFu : weight_order(p.weight[at]);
+    const float w = p.weight[at];
+    return p.position[at] >= recent ? 0xFFFFFFFFu : weight_order(w);
   };
-  const int held = min(L, p.smem_keys);
-  for (int r = threadIdx.x; r < held; r += kSelectThreads) s_key[r] = compute(r);
-  auto key = [&](int r) { return r < held ? s_key[r] : compute(r); };
+  const int held = min(mine, p.smem_keys);
+#pragma unroll 4
+  for (int i = tid; i < held; i += kSelectThreads) s_key[i] = compute(i);
+  auto key = [&](int i) { return i < held ? s_key[i] : compute(i); };
+  __syncthreads();
 
-  // Radix selection of the n_keep-th largest key: digits of 11, 11 and 10
-  // bits from the top. `want` keys are still to be found below the prefix.
+  // `want` keys are still to be found among those that start with `prefix`.
   uint32_t prefix = 0u;
   int want = p.n_keep;
   for (int d = 0; d < 3; ++d) {
     const int shift = d == 0 ? 21 : (d == 1 ? 10 : 0);
-    const int bins = d == 2 ? 1024 : 2048;
-    for (int i = threadIdx.x; i < 2048; i += kSelectThreads) s_hist[i] = 0u;
-    __syncthreads();
-    for (int r0 = 0; r0 < L; r0 += kSelectThreads) {
-      const int r = r0 + threadIdx.x;
-      const uint32_t k = r < L ? key(r) : 0u;
-      const bool in = r < L && (d == 0 || (k >> (d == 1 ? 21 : 10)) == prefix);
-      const uint32_t digit = in ? ((k >> shift) & (bins - 1)) : 0xFFFFFFFFu;
-      const uint32_t same = __match_any_sync(0xffffffffu, digit);
-      if (in && lane == __ffs(same) - 1) atomicAdd(&s_hist[digit], __popc(same));
+    uint32_t* hist = s_hist[d & 1];
+    for (int i0 = 0; i0 < mine; i0 += kSelectThreads) {
+      const int i = i0 + tid;
+      const uint32_t k = i < mine ? key(i) : 0u;
+      const bool in = i < mine && (d == 0 || (k >> (d == 1 ? 21 : 10)) == prefix);
+      const uint32_t digit = (k >> shift) & (d == 2 ? 1023u : 2047u);
+      // Equal weights (rows never attended to) are common: the lanes that
+      // agree with the first counting one add once.
+      const uint32_t m = __ballot_sync(0xffffffffu, in);
+      if (m == 0u) continue;
+      const int head_lane = __ffs(m) - 1;
+      const uint32_t first_digit = __shfl_sync(0xffffffffu, digit, head_lane);
+      const uint32_t same = __ballot_sync(0xffffffffu, in && digit == first_digit);
+      if (lane == head_lane) atomicAdd(&hist[digit], __popc(same));
+      else if (in && !((same >> lane) & 1u)) atomicAdd(&hist[digit], 1u);
     }
-    __syncthreads();
-    // Suffix sums from the top bin: thread t holds bins 2t and 2t + 1.
-    const uint32_t h0 = s_hist[2 * threadIdx.x], h1 = s_hist[2 * threadIdx.x + 1];
-    uint32_t inc = h0 + h1;  // inclusive suffix sum over threads t .. 1023
+    cluster_sync();
+    // Thread t holds bins 2t and 2t + 1 of all CTAs; suffix sums from the top.
+    uint32_t h0 = 0u, h1 = 0u;
+    if (ranks == 1) {
+      h0 = hist[2 * tid];
+      h1 = hist[2 * tid + 1];
+    } else {
+      for (int k = 0; k < ranks; ++k) {
+        h0 += peer_load(&hist[2 * tid], k);
+        h1 += peer_load(&hist[2 * tid + 1], k);
+      }
+    }
+    uint32_t inc = h0 + h1;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint32_t t = __shfl_down_sync(0xffffffffu, inc, o);
       if (lane + o < 32) inc += t;
     }
-    if (lane == 0) s_warp[0][warp] = static_cast<int>(inc);
+    if (lane == 0) s_warp[warp] = inc;
     __syncthreads();
-    for (int w = warp + 1; w < 32; ++w) inc += static_cast<uint32_t>(s_warp[0][w]);
+    uint32_t later = s_warp[lane];  // of the warps behind this one
+    later = lane > warp ? later : 0u;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) later += __shfl_xor_sync(0xffffffffu, later, o);
+    inc += later;
     const uint32_t above = inc - h0 - h1;  // keys in bins over 2t + 1
     if (above < static_cast<uint32_t>(want) && inc >= static_cast<uint32_t>(want)) {
       const bool top = above + h1 >= static_cast<uint32_t>(want);
-      s_pick[0] = 2 * threadIdx.x + (top ? 1 : 0);
+      s_pick[0] = 2 * tid + (top ? 1 : 0);
       s_pick[1] = static_cast<uint32_t>(want) - above - (top ? 0u : h1);
     }
     __syncthreads();
     prefix = d == 0 ? s_pick[0] : ((prefix << (d == 1 ? 11 : 10)) | s_pick[0]);
     want = static_cast<int>(s_pick[1]);
+    // The buffer of pass 0 serves pass 2: cleared here, while no CTA reads it
+    // any more (all have passed the meeting of pass 1).
+    if (d == 1) {
+      for (int i = tid; i < kBins; i += kSelectThreads) s_hist[0][i] = 0u;
+      __syncthreads();
+    }
   }
   // Kept: keys above `prefix`, and the first `want` rows equal to it. Each
-  // warp takes a run of consecutive rows and counts before it writes.
-  const int seg = ((L + 31) / 32 + 31) / 32 * 32;
-  const int r_lo = min(L, warp * seg), r_hi = min(L, r_lo + seg);
-  auto warp_prefix = [&](int which, int mine, int& before) {
-    if (lane == 0) s_warp[which][warp] = mine;
+  // warp takes a run of consecutive rows and counts before it writes; a
+  // count's place is what the warps and the CTAs before it have.
+  const int seg = ((mine + 31) / 32 + 31) / 32 * 32;
+  const int i_lo = min(mine, warp * seg), i_hi = min(mine, i_lo + seg);
+  auto before_warp = [&](uint32_t count, uint32_t& total) -> uint32_t {
     __syncthreads();
-    const int x = s_warp[which][lane];
-    before = 0;
-    int total = 0;
-    for (int w = 0; w < 32; ++w) {
-      const int y = __shfl_sync(0xffffffffu, x, w);
-      if (w < warp) before += y;
-      total += y;
+    if (lane == 0) s_warp[warp] = count;
+    __syncthreads();
+    const uint32_t x = s_warp[lane];
+    uint32_t inc = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
     }
-    return total;
+    total = __shfl_sync(0xffffffffu, inc, 31);
+    return __shfl_sync(0xffffffffu, inc - x, warp);
   };
-  int eq = 0;
-  for (int r0 = r_lo; r0 < r_hi; r0 += 32)
-    eq += __popc(__ballot_sync(0xffffffffu, r0 + lane < r_hi && key(r0 + lane) == prefix));
-  int eq_before;
-  warp_prefix(0, eq, eq_before);
+  auto before_cta = [&](int which, uint32_t& total) -> uint32_t {  // after the counts have met
+    uint32_t sum = 0u;
+    total = 0u;
+    for (int k = 0; k < ranks; ++k) {
+      const uint32_t x = ranks == 1 ? s_count[which] : peer_load(&s_count[which], k);
+      if (k < rank) sum += x;
+      total += x;
+    }
+    return sum;
+  };
   const uint32_t below = (1u << lane) - 1u;
-  int holes = 0, movers = 0, hole_at = 0, mover_at = 0, total = 0;
+  uint32_t eq = 0u, cta_total, all;
+  for (int i0 = i_lo; i0 < i_hi; i0 += 32)
+    eq += __popc(__ballot_sync(0xffffffffu, i0 + lane < i_hi && key(i0 + lane) == prefix));
+  uint32_t eq_before = before_warp(eq, cta_total);
+  if (tid == 0) s_count[0] = cta_total;
+  cluster_sync();
+  eq_before += before_cta(0, all);
+  uint32_t hole_at = 0u, mover_at = 0u, total = 0u;
   for (int pass = 0; pass < 2; ++pass) {
-    int e = eq_before;
-    int nh = hole_at, nm = mover_at;
-    for (int r0 = r_lo; r0 < r_hi; r0 += 32) {
-      const int r = r0 + lane;
-      const bool in = r < r_hi;
-      const uint32_t k = in ? key(r) : 0u;
+    uint32_t e = eq_before, nh = hole_at, nm = mover_at;
+    for (int i0 = i_lo; i0 < i_hi; i0 += 32) {
+      const int i = i0 + lane, r = base + i;
+      const bool in = i < i_hi;
+      const uint32_t k = in ? key(i) : 0u;
       const uint32_t tie = __ballot_sync(0xffffffffu, in && k == prefix);
-      const bool kept = in && (k > prefix || (k == prefix && e + __popc(tie & below) < want));
+      const bool kept =
+          in && (k > prefix || (k == prefix && e + __popc(tie & below) < static_cast<uint32_t>(want)));
       e += __popc(tie);
       const bool hole = in && !kept && r < p.n_keep, mover = kept && r >= p.n_keep;
       const uint32_t mh = __ballot_sync(0xffffffffu, hole), mm = __ballot_sync(0xffffffffu, mover);
@@ -154,14 +218,19 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectPara
       nm += __popc(mm);
     }
     if (pass == 0) {
-      holes = nh;
-      movers = nm;
-      warp_prefix(1, holes, hole_at);
-      total = warp_prefix(2, movers, mover_at);
+      hole_at = before_warp(nh, cta_total);
+      if (tid == 0) s_count[1] = cta_total;
+      mover_at = before_warp(nm, cta_total);
+      if (tid == 0) s_count[2] = cta_total;
+      cluster_sync();
+      hole_at += before_cta(1, all);
+      mover_at += before_cta(2, total);
     }
   }
-  if (threadIdx.x == 0) p.n_moves[head] = total;
-  for (int i = total + threadIdx.x; i < p.n_keep; i += kSelectThreads) src[i] = dst[i] = -1;
+  if (lead && tid == 0) p.n_moves[head] = static_cast<int>(total);
+  for (int i = static_cast<int>(total) + rank * kSelectThreads + tid; i < p.n_keep; i += ranks * kSelectThreads)
+    src[i] = dst[i] = -1;
+  cluster_sync();  // no CTA leaves while another may still read its counts
 }
 
 struct MoveParams {
@@ -174,11 +243,15 @@ struct MoveParams {
 };
 
 constexpr int kMoveThreads = 256;
+constexpr int kMoveCtas = 8 * kSMs;  // of a call, about: a head's moves are spread over its share of them
+constexpr int kMoveBatch = 4;        // moves a group of lanes has in flight
 
-// D / 8 lanes copy one row of K and of V, 16 bytes each.
+// D / 8 lanes copy one row of K and of V, 16 bytes each, kMoveBatch rows at a
+// time: the rows lie anywhere, so what counts is how many loads are in
+// flight behind the three dependent ones (move, page, row).
 template <int D>
 __global__ void __launch_bounds__(kMoveThreads) move_kernel(const MoveParams p) {
-  constexpr int LPR = D / 8, RPP = kMoveThreads / LPR;
+  constexpr int LPR = D / 8, GPC = kMoveThreads / LPR;
   const View& v = p.v;
   const int hk = blockIdx.y, b = blockIdx.z;
   pdl_launch_dependents();
@@ -190,24 +263,51 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const MoveParams p) 
     return;
   }
   const int sub = threadIdx.x % LPR;
-  for (int i = blockIdx.x * RPP + threadIdx.x / LPR; i < n; i += gridDim.x * RPP) {
-    const int from = p.src[head * p.stride + i], to = p.dst[head * p.stride + i];
-    if (from < 0 || from >= v.T || to < 0 || to >= v.T) {
-      if (sub == 0) atomicOr(&g_status, kStatusRange);
-      continue;
+  for (int i0 = (blockIdx.x * GPC + threadIdx.x / LPR) * kMoveBatch; i0 < n; i0 += gridDim.x * GPC * kMoveBatch) {
+    int from[kMoveBatch], to[kMoveBatch], pf[kMoveBatch], pt[kMoveBatch];
+#pragma unroll
+    for (int j = 0; j < kMoveBatch; ++j) {
+      const bool in = i0 + j < n;
+      from[j] = in ? p.src[head * p.stride + i0 + j] : 0;
+      to[j] = in ? p.dst[head * p.stride + i0 + j] : 0;
     }
-    const int pf = page_at(v, b, from / v.page_size), pt = page_at(v, b, to / v.page_size);
-    if (pf < 0 || pt < 0) continue;
-    const size_t a = kv_index(v, pf, from % v.page_size, hk) * D + sub * 8;
-    const size_t z = kv_index(v, pt, to % v.page_size, hk) * D + sub * 8;
-    const uint4 kk = *reinterpret_cast<const uint4*>(p.k_pages + a);
-    const uint4 vv = *reinterpret_cast<const uint4*>(p.v_pages + a);
-    *reinterpret_cast<uint4*>(p.k_pages + z) = kk;
-    *reinterpret_cast<uint4*>(p.v_pages + z) = vv;
-    if (sub == 0) {
-      const size_t ta = term_index(v, pf, from % v.page_size, hk), tz = term_index(v, pt, to % v.page_size, hk);
-      p.weight[tz] = p.weight[ta];
-      p.position[tz] = p.position[ta];
+#pragma unroll
+    for (int j = 0; j < kMoveBatch; ++j) {
+      pf[j] = pt[j] = -1;
+      if (i0 + j >= n) continue;
+      if (from[j] < 0 || from[j] >= v.T || to[j] < 0 || to[j] >= v.T) {
+        atomicOr(&g_status, kStatusRange);
+        continue;
+      }
+      pf[j] = page_at(v, b, from[j] / v.page_size);
+      pt[j] = page_at(v, b, to[j] / v.page_size);
+    }
+    uint4 kk[kMoveBatch], vv[kMoveBatch];
+    float w[kMoveBatch];
+    int pos[kMoveBatch];
+#pragma unroll
+    for (int j = 0; j < kMoveBatch; ++j) {
+      if (pf[j] < 0 || pt[j] < 0) continue;
+      const int slot = from[j] % v.page_size;
+      const size_t a = kv_index(v, pf[j], slot, hk) * D + sub * 8;
+      kk[j] = *reinterpret_cast<const uint4*>(p.k_pages + a);
+      vv[j] = *reinterpret_cast<const uint4*>(p.v_pages + a);
+      if (sub == 0) {
+        w[j] = p.weight[term_index(v, pf[j], slot, hk)];
+        pos[j] = p.position[term_index(v, pf[j], slot, hk)];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kMoveBatch; ++j) {
+      if (pf[j] < 0 || pt[j] < 0) continue;
+      const int slot = to[j] % v.page_size;
+      const size_t z = kv_index(v, pt[j], slot, hk) * D + sub * 8;
+      *reinterpret_cast<uint4*>(p.k_pages + z) = kk[j];
+      *reinterpret_cast<uint4*>(p.v_pages + z) = vv[j];
+      if (sub == 0) {
+        p.weight[term_index(v, pt[j], slot, hk)] = w[j];
+        p.position[term_index(v, pt[j], slot, hk)] = pos[j];
+      }
     }
   }
 }

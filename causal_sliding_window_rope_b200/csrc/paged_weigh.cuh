@@ -218,7 +218,7 @@ struct WeighTileParams {
   unsigned long long wait_ns;
 };
 
-constexpr int kWeighThreads = 192;  // producer, MMA issuer, 4 warps of sums
+constexpr int kWeighThreads = 320;  // producer, MMA issuer, 8 warps of sums
 constexpr int kWeighCluster = 4;    // CTAs that may share a unit's query tiles
 constexpr int kWeighCtas = 2 * kSMs;  // two per SM: one's products and copies under the other's sums
 constexpr int kWeighWhole = 6;      // units per CTA from which each takes whole ones
@@ -230,7 +230,8 @@ struct WeighTileSmem {
   static constexpr int kOffQ = kOp;                 // 2 slots
   static constexpr int kOffLse = 3 * kOp;           // [2][128] float
   static constexpr int kOffSum = kOffLse + 1024;    // [2][kWeighCluster - 1][128] float: the other CTAs' sums
-  static constexpr int kOffBar = kOffSum + 2 * (kWeighCluster - 1) * 512;
+  static constexpr int kOffHalf = kOffSum + 2 * (kWeighCluster - 1) * 512;  // [128] float: the second half's sums
+  static constexpr int kOffBar = kOffHalf + 512;
   static constexpr int kOffPre = kOffBar + 8 * 18;  // int [B + 1]
   static constexpr int kBytes = kOffPre + 1024;     // and 4 (B + 1) more; two CTAs fit an SM
   static_assert(kBytes + 4 * (kMaxSeqs + 1) <= 232448, "shared memory per block");
@@ -278,7 +279,7 @@ __global__ void __launch_bounds__(kWeighThreads, 2) __cluster_dims__(kWeighClust
   uint64_t* q_full = k_full + 2;    // [2]
   uint64_t* q_empty = k_full + 4;   // [2]
   uint64_t* s_full = k_full + 6;    // [2] S^T buffers
-  uint64_t* s_empty = k_full + 8;   // [2] (128 arrivals)
+  uint64_t* s_empty = k_full + 8;   // [2] (256 arrivals)
   uint64_t* mma_done = k_full + 10;
   uint64_t* sum_full = k_full + 11;  // [2] rank 0: the others' sums have come
   uint64_t* sum_free = k_full + 13;  // [2] the others: rank 0 has read the buffer
@@ -295,7 +296,7 @@ __global__ void __launch_bounds__(kWeighThreads, 2) __cluster_dims__(kWeighClust
       mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], 1);
       mbar_init(&s_full[i], 1);
-      mbar_init(&s_empty[i], 128);
+      mbar_init(&s_empty[i], 256);
       mbar_init(&sum_full[i], 128 * (kWeighCluster - 1));
       mbar_init(&sum_free[i], 1);
     }
@@ -456,8 +457,10 @@ __global__ void __launch_bounds__(kWeighThreads, 2) __cluster_dims__(kWeighClust
       drain_wait(mma_done, 0);
     }
   } else {
-    // ---------------------------------------------------- sums: thread = cached row
-    const int quad = warp & 3, r = quad * 32 + lane;
+    // ---------------------------------------------------- sums: two threads per cached row
+    // Warps 2-5 take columns 0-63 of each tile, warps 6-9 columns 64-127.
+    const int quad = warp & 3, r = quad * 32 + lane, half = warp >= 6 ? 1 : 0;
+    float* s_half = reinterpret_cast<float*>(smem + SM::kOffHalf);
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
     const float c2 = p.scale_log2;
     int nq = 0, nu = 0;
@@ -473,12 +476,14 @@ __global__ void __launch_bounds__(kWeighThreads, 2) __cluster_dims__(kWeighClust
                    ? p.lse[static_cast<size_t>(x.s.tok0 + i) * v.H + x.hk * v.g + r % v.g] * -1.4426950408889634f
                    : 0.f;
       };
-      float term = row_term(x.q0);
+      float term = half == 0 ? row_term(x.q0) : 0.f;
       for (int q = x.q0; ok && q <= x.q1; q += ranks, ++nq) {
         const int buf = nq & 1, i0 = q * p.tpt;
-        s_lse[buf * 128 + r] = term;
-        term = row_term(q + ranks);  // the next tile's, under this one's sums
-        ok = named_bar_and(1, 128, mbar_wait(&s_full[buf], (nq >> 1) & 1, wc));
+        if (half == 0) {
+          s_lse[buf * 128 + r] = term;
+          term = row_term(q + ranks);  // the next tile's, under this one's sums
+        }
+        ok = named_bar_and(1, 256, mbar_wait(&s_full[buf], (nq >> 1) & 1, wc));
         if (!ok) break;
         tc_fence_after();
         // Columns [a, b] are the query rows that see this cached row:
@@ -490,7 +495,8 @@ __global__ void __launch_bounds__(kWeighThreads, 2) __cluster_dims__(kWeighClust
         const int b = static_cast<int>(min(static_cast<long long>(cols) - 1, hi_col));
         float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
+        for (int h2 = 0; h2 < 2; ++h2) {
+          const int h = 2 * half + h2;
           if (!__any_sync(0xffffffffu, a <= 32 * h + 31 && b >= 32 * h)) continue;  // nobody sees these
           uint32_t sv[32];
           tmem_ld32(tmem + lane_off + buf * 128 + h * 32, sv);
@@ -522,28 +528,35 @@ __global__ void __launch_bounds__(kWeighThreads, 2) __cluster_dims__(kWeighClust
         mbar_arrive(&s_empty[buf]);
       }
       if (!ok) break;
-      if (shared) {
+      // The two halves of a row meet; warps 2-5 go on with its sum.
+      if (half == 1) s_half[r] = total;
+      named_bar(1, 256);
+      if (half == 0) {
+        total += s_half[r];
         const int buf = nu & 1;
         float* slot = s_sum + buf * (kWeighCluster - 1) * 128 + r;
-        if (rank > 0) {
-          ok = named_bar_and(1, 128, nu < 2 || mbar_wait(&sum_free[buf], ((nu >> 1) - 1) & 1, wc));
-          if (!ok) break;
-          asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr(slot + (rank - 1) * 128, 0)), "f"(total)
-                       : "memory");
-          cluster_arrive(cluster_addr(&sum_full[buf], 0));
-          continue;
-        }
-        ok = named_bar_and(1, 128, cluster_wait(&sum_full[buf], (nu >> 1) & 1, wc));
-        if (!ok) break;
+        if (shared && rank > 0) {
+          ok = named_bar_and(2, 128, nu < 2 || mbar_wait(&sum_free[buf], ((nu >> 1) - 1) & 1, wc));
+          if (ok) {
+            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr(slot + (rank - 1) * 128, 0)), "f"(total)
+                         : "memory");
+            cluster_arrive(cluster_addr(&sum_full[buf], 0));
+          }
+        } else if (shared) {
+          ok = named_bar_and(2, 128, cluster_wait(&sum_full[buf], (nu >> 1) & 1, wc));
+          if (ok) {
 #pragma unroll
-        for (int k = 0; k < kWeighCluster - 1; ++k) total += slot[k * 128];
-        named_bar(1, 128);  // every thread has read the buffer
-        if (r > 0 && r < kWeighCluster) cluster_arrive(cluster_addr(&sum_free[buf], r));
+            for (int k = 0; k < kWeighCluster - 1; ++k) total += slot[k * 128];
+            named_bar(2, 128);  // every thread has read the buffer
+            if (r > 0 && r < kWeighCluster) cluster_arrive(cluster_addr(&sum_free[buf], r));
+          }
+        }
+        if (ok && rank == 0 && mine) {
+          const int page = page_at(v, x.b, key / v.page_size);
+          if (page >= 0) p.weight[term_index(v, page, key % v.page_size, x.hk)] += total;
+        }
       }
-      if (mine) {
-        const int page = page_at(v, x.b, key / v.page_size);
-        if (page >= 0) p.weight[term_index(v, page, key % v.page_size, x.hk)] += total;
-      }
+      ok = named_bar_and(1, 256, ok);  // all leave together when a wait ran out
     }
   }
   __syncwarp();
