@@ -35,8 +35,8 @@ EXPORTS = ("attn_prologue", "attn_prologue_gated", "attn_gate_bwd", "attn_qkv_pr
            "attn_qkv_fp8_workspace_bytes", "attn_qkv_prologue_fp8", "attn_qkv_bwd", "attn_fwd",
            "attn_bwd_workspace_bytes", "attn_bwd", "attn_bwd_noalloc",
            "attn_decode_workspace_bytes", "attn_decode", "attn_paged_append",
-           "attn_paged_workspace_bytes", "attn_paged", "attn_paged_weigh", "attn_paged_select",
-           "attn_paged_move", "cswattn_gemm_bf16",
+           "attn_paged_workspace_bytes", "attn_paged", "attn_paged_weigh",
+           "attn_paged_weigh_workspace_bytes", "attn_paged_select", "attn_paged_move", "cswattn_gemm_bf16",
            "muon_ns_workspace_bytes", "muon_newton_schulz",
            "cswattn_sync_status", "cswattn_set_wait_limit_ns", "cswattn_set_timing",
            "cswattn_kernel_times", "cswattn_selftest_wait_timeout", "cswattn_last_error",
@@ -128,7 +128,9 @@ def lib():
         L.attn_paged_workspace_bytes.argtypes = [lp, pp]
         L.attn_paged_workspace_bytes.restype = sz
         L.attn_paged.argtypes = [lp, pp] + [vp] * 6 + [sz, vp]
-        L.attn_paged_weigh.argtypes = [lp, pp] + [vp] * 5
+        L.attn_paged_weigh.argtypes = [lp, pp] + [vp] * 5 + [sz, vp]
+        L.attn_paged_weigh_workspace_bytes.argtypes = [lp, pp]
+        L.attn_paged_weigh_workspace_bytes.restype = sz
         L.attn_paged_select.argtypes = [lp, pp] + [vp] * 3 + [ci, ci] + [vp] * 5
         L.attn_paged_move.argtypes = [lp, pp] + [vp] * 3 + [ci] + [vp] * 5
         for name in ("attn_paged_append", "attn_paged", "attn_paged_weigh", "attn_paged_select",
@@ -515,14 +517,33 @@ def attn_paged(spec: LayerSpec, batch: PagedBatch, cache: PagedCache, q_out, O, 
                 workspace.data_ptr(), workspace_bytes)
 
 
-def attn_paged_weigh(spec: LayerSpec, batch: PagedBatch, cache: PagedCache, q_out, lse, stream=None):
-    """Adds the new tokens' attention weights to cache.weight."""
+def attn_paged_weigh_workspace_bytes(spec: LayerSpec, batch: PagedBatch, cache: PagedCache) -> int:
+    """Scratch bytes of attn_paged_weigh; 0 for a call of few query rows."""
+    return int(lib().attn_paged_weigh_workspace_bytes(ctypes.byref(spec.c()), ctypes.byref(batch.c(spec, cache))))
+
+
+def attn_paged_weigh(spec: LayerSpec, batch: PagedBatch, cache: PagedCache, q_out, lse, workspace=None, stream=None):
+    """Adds the new tokens' attention weights to cache.weight. workspace:
+    attn_paged_weigh_workspace_bytes of scratch; None: a call that needs some
+    takes it from PyTorch's allocator on its stream."""
     import torch
     N, H, dev = batch.n_tokens, spec.n_head, batch.device
     _want(dev, ("q_out", q_out, (N, H, spec.head_dim), torch.bfloat16), ("lse", lse, (N, H), torch.float32))
     k, weight = cache.need(spec, dev, "k", "weight")
-    _paged_call(lib().attn_paged_weigh, dev, stream, ctypes.byref(spec.c()), ctypes.byref(batch.c(spec, cache)),
-                q_out.data_ptr(), k, lse.data_ptr(), weight)
+    layer, paged = ctypes.byref(spec.c()), ctypes.byref(batch.c(spec, cache))
+    if workspace is not None:
+        _want(dev, ("workspace", workspace, workspace.shape, workspace.dtype))
+    elif batch.max_new * H > 8 * spec.n_kv_head:  # else none is needed, whatever the sizes
+        nbytes = int(lib().attn_paged_weigh_workspace_bytes(layer, paged))
+        if nbytes:
+            if stream is None:
+                workspace = torch.empty(nbytes, dtype=torch.uint8, device=batch.page_table.device)
+            else:
+                s = torch.cuda.ExternalStream(stream, dev) if isinstance(stream, int) else stream
+                with torch.cuda.stream(s):  # freed memory is reused in this stream's order
+                    workspace = torch.empty(nbytes, dtype=torch.uint8, device=batch.page_table.device)
+    _paged_call(lib().attn_paged_weigh, dev, stream, layer, paged, q_out.data_ptr(), k, lse.data_ptr(), weight,
+                _at(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size())
 
 
 def attn_paged_select(spec: LayerSpec, batch: PagedBatch, cache: PagedCache, next_pos, n_keep, n_recent, n_moves,

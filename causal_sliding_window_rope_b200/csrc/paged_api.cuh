@@ -132,54 +132,95 @@ cswattn_status make_map_group(CUtensorMap* map, const void* base, int n_tokens, 
   return CSWATTN_OK;
 }
 
-// The kernels of many query rows: the deal, the tiles, the join of what was cut.
-template <int D>
-void launch_tile_kernels(const paged::TileParams& tp, paged::Plan* plan, int* longs, const CUtensorMap& mq,
-                         const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t st) {
-  launch_pdl(paged::plan_kernel, dim3(1), dim3(paged::kPlanThreads), 0, st, tp.v, tp.tpt, tp.short_rows, plan, longs);
-  launch_pdl(paged::tile_kernel<D>, dim3(paged::kSMs), dim3(paged::kTileThreads), paged::TileSmem<D>::kBytes, st, mq,
-             mk, mv, tp);
-  launch_pdl(paged::tile_combine_kernel<D>, dim3(paged::kSMs - 1, 256 / paged::kTileCombineRows),
-             dim3(32 * paged::kTileCombineRows), 0, st, tp);
+template <int D, int MB>
+cswattn_status prepare_rows_kernel() {
+  return set_smem(paged::rows_kernel<D, MB>, paged::RowsSmem<D, MB>::kBytes + 4 * (paged::kMaxSeqs + 1));
+}
+template <int D, int MB>
+void launch_rows_kernel(const paged::RowsParams& rp, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t st) {
+  launch_pdl(paged::rows_kernel<D, MB>, dim3(paged::kSMs), dim3(32 * (paged::kKeyGroups * MB + 1)),
+             static_cast<size_t>(paged::RowsSmem<D, MB>::kBytes) + 4 * (rp.v.B + 1), st, mk, mv, rp);
 }
 
-// The kernel of few query rows and, behind it, the join of what it cut.
-template <int D, int MB>
-cswattn_status launch_rows_kernel(const paged::RowsParams& rp, const CUtensorMap& mk, const CUtensorMap& mv,
-                                  cudaStream_t st) {
-  using SM = paged::RowsSmem<D, MB>;
-  cswattn_status e = set_smem(paged::rows_kernel<D, MB>, SM::kBytes + 4 * (paged::kMaxSeqs + 1));
-  if (e != CSWATTN_OK) return e;
-  launch_pdl(paged::rows_kernel<D, MB>, dim3(paged::kSMs), dim3(32 * (paged::kKeyGroups * MB + 1)),
-             static_cast<size_t>(SM::kBytes) + 4 * (rp.v.B + 1), st, mk, mv, rp);
-  paged::CombineParams cp;
-  cp.v = rp.v;
-  cp.max_rows = 16 * MB;
-  cp.slot_rows = 16 * MB;
-  cp.part_o = rp.part_o;
-  cp.part_ml = rp.part_ml;
-  cp.info = rp.info;
-  cp.O = rp.O;
-  cp.lse = rp.lse;
-  launch_pdl(paged::combine_kernel<D>, dim3(static_cast<unsigned>(rp.v.B) * rp.v.Hk), dim3(paged::kCombineThreads), 0,
-             st, cp);
+// The attention of few query rows, that of many, and the join of what both have cut. With prepare_only, sets
+// what the launches need: a call that may fail is made before anything of an
+// entry point is enqueued.
+template <int D>
+cswattn_status launch_paged(const paged::RowsParams& rp, const paged::TileParams& tp, const paged::JoinParams& jp,
+                            bool tiles, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mq,
+                            const CUtensorMap& mk128, const CUtensorMap& mv128, cudaStream_t st, bool prepare_only) {
+  const bool wide = jp.max_rows > 16;
+  if (prepare_only) {
+    cswattn_status e = wide ? prepare_rows_kernel<D, 2>() : prepare_rows_kernel<D, 1>();
+    if (e != CSWATTN_OK || !tiles) return e;
+    return set_smem(paged::tile_kernel<D>, paged::TileSmem<D>::kBytes);
+  }
+  if (wide) launch_rows_kernel<D, 2>(rp, mk, mv, st);
+  else launch_rows_kernel<D, 1>(rp, mk, mv, st);
+  if (tiles)
+    launch_pdl(paged::tile_kernel<D>, dim3(paged::kSMs), dim3(paged::kTileThreads), paged::TileSmem<D>::kBytes, st,
+               mq, mk128, mv128, tp);
+  const unsigned cuts = tiles ? (paged::kSMs - 1) * (256 / paged::kJoinWarps) : 0;
+  launch_pdl(paged::join_kernel<D>, dim3(static_cast<unsigned>(rp.v.B) * rp.v.Hk + cuts),
+             dim3(32 * paged::kJoinWarps), 0, st, jp);
   return CSWATTN_OK;
 }
 
+struct WeighWorkspace {
+  paged::Plan* plan;
+  int* longs;
+  float* part;
+  int max_rows;  // query rows of a sequence that the kernel of few takes
+  bool tiles;    // a sequence may have more
+  size_t bytes;
+};
+
+WeighWorkspace carve_weigh(const Shape& s, const paged::View& v, void* base) {
+  uint8_t* p = static_cast<uint8_t*>(base);
+  WeighWorkspace w;
+  const long long rows = static_cast<long long>(v.max_new) * s.g;
+  w.max_rows = rows <= 8 ? 8 : (rows <= 16 ? 16 : 32);
+  w.tiles = rows > w.max_rows;
+  w.plan = nullptr;
+  w.longs = nullptr;
+  w.part = nullptr;
+  w.bytes = 0;
+  if (!w.tiles) return w;
+  size_t off = 0;
+  w.plan = reinterpret_cast<paged::Plan*>(p + off);
+  off += pad256(sizeof(paged::Plan));
+  w.longs = reinterpret_cast<int*>(p + off);
+  off += pad256(static_cast<size_t>(s.B) * 4);
+  w.part = reinterpret_cast<float*>(p + off);
+  off += pad256(static_cast<size_t>(2 * paged::kWeighRuns) * 128 * 4);
+  w.bytes = off;
+  return w;
+}
+
 template <int D, int NT>
-cswattn_status launch_weigh_rows_nt(const paged::WeighRowsParams& rp, const CUtensorMap& mk, cudaStream_t st) {
+cswattn_status launch_weigh_rows(const paged::WeighRowsParams& rp, const CUtensorMap& mk, cudaStream_t st,
+                                 bool prepare_only) {
   using SM = paged::WeighRowsSmem<D>;
-  cswattn_status e = set_smem(paged::weigh_rows_kernel<D, NT>, SM::kBytes + 4 * (paged::kMaxSeqs + 1));
-  if (e != CSWATTN_OK) return e;
+  if (prepare_only) return set_smem(paged::weigh_rows_kernel<D, NT>, SM::kBytes + 4 * (paged::kMaxSeqs + 1));
   launch_pdl(paged::weigh_rows_kernel<D, NT>, dim3(paged::kSMs), dim3(32 * (4 * paged::kWeighGroups + 1)),
              static_cast<size_t>(SM::kBytes) + 4 * (rp.v.B + 1), st, mk, rp);
   return CSWATTN_OK;
 }
+
+// As launch_paged, for the row weights.
 template <int D>
-cswattn_status launch_weigh_rows(const paged::WeighRowsParams& rp, const CUtensorMap& mk, cudaStream_t st) {
-  return rp.max_rows == 8    ? launch_weigh_rows_nt<D, 1>(rp, mk, st)
-         : rp.max_rows == 16 ? launch_weigh_rows_nt<D, 2>(rp, mk, st)
-                             : launch_weigh_rows_nt<D, 4>(rp, mk, st);
+cswattn_status launch_weigh(const paged::WeighRowsParams& rp, const paged::WeighTileParams& tp, bool tiles,
+                            const CUtensorMap& mk, const CUtensorMap& mq, const CUtensorMap& mk128, cudaStream_t st,
+                            bool prepare_only) {
+  cswattn_status e = rp.max_rows == 8    ? launch_weigh_rows<D, 1>(rp, mk, st, prepare_only)
+                     : rp.max_rows == 16 ? launch_weigh_rows<D, 2>(rp, mk, st, prepare_only)
+                                         : launch_weigh_rows<D, 4>(rp, mk, st, prepare_only);
+  if (e != CSWATTN_OK || !tiles) return e;
+  if (prepare_only) return set_smem(paged::weigh_tile_kernel<D>, paged::WeighTileSmem<D>::kBytes);
+  launch_pdl(paged::weigh_tile_kernel<D>, dim3(paged::kWeighRuns), dim3(paged::kWeighThreads),
+             paged::WeighTileSmem<D>::kBytes, st, mq, mk128, tp);
+  launch_pdl(paged::weigh_join_kernel, dim3(paged::kWeighRuns - 1), dim3(128), 0, st, tp);
+  return CSWATTN_OK;
 }
 
 }  // namespace
@@ -301,46 +342,61 @@ cswattn_status attn_paged(const cswattn_layer* layer, const cswattn_paged* paged
   rp.part_ml = w.part_ml;
   rp.info = w.info;
   rp.wait_ns = g_wait_ns.load();
-  CUtensorMap mk, mv;
+  paged::TileParams tp;
+  tp.v = v;
+  tp.scale_log2 = rp.scale_log2;
+  tp.unit = page_unit(v.page_size, 128);
+  tp.tpt = 128 / s.g;
+  tp.short_rows = w.slot_rows;
+  tp.plan = w.plan;
+  tp.longs = w.longs;
+  tp.O = rp.O;
+  tp.lse = lse;
+  tp.part_o = w.tile_o;
+  tp.part_ml = w.tile_ml;
+  tp.wait_ns = rp.wait_ns;
+  paged::JoinParams jp;
+  jp.v = v;
+  jp.max_rows = w.slot_rows;
+  jp.part_o = w.part_o;
+  jp.part_ml = w.part_ml;
+  jp.info = w.info;
+  jp.tpt = tp.tpt;
+  jp.plan = w.plan;
+  jp.longs = w.longs;
+  jp.tile_o = w.tile_o;
+  jp.tile_ml = w.tile_ml;
+  jp.O = rp.O;
+  jp.lse = lse;
+  // What may fail is done before anything is enqueued.
+  CUtensorMap mk, mv, mq, mk128, mv128;
   if ((st = make_map(&mk, k_pages, v.n_pages, v.page_size, s.Hk, rp.unit, s.D)) != CSWATTN_OK) return st;
   if ((st = make_map(&mv, v_pages, v.n_pages, v.page_size, s.Hk, rp.unit, s.D)) != CSWATTN_OK) return st;
-  // What may fail is done before anything is enqueued.
-  CUtensorMap mq, mk128, mv128;
-  paged::TileParams tp;
   if (w.tiles) {
-    tp.v = v;
-    tp.scale_log2 = rp.scale_log2;
-    tp.unit = page_unit(v.page_size, 128);
-    tp.tpt = 128 / s.g;
-    tp.short_rows = w.slot_rows;
-    tp.plan = w.plan;
-    tp.longs = w.longs;
-    tp.O = rp.O;
-    tp.lse = lse;
-    tp.part_o = w.tile_o;
-    tp.part_ml = w.tile_ml;
-    tp.wait_ns = rp.wait_ns;
     if ((st = make_map_group(&mq, q_out, v.n_tokens, s.H, s.D, s.g, tp.tpt)) != CSWATTN_OK) return st;
     if ((st = make_map(&mk128, k_pages, v.n_pages, v.page_size, s.Hk, tp.unit, s.D)) != CSWATTN_OK) return st;
     if ((st = make_map(&mv128, v_pages, v.n_pages, v.page_size, s.Hk, tp.unit, s.D)) != CSWATTN_OK) return st;
-    st = s.D == 64 ? set_smem(paged::tile_kernel<64>, paged::TileSmem<64>::kBytes)
-                   : set_smem(paged::tile_kernel<128>, paged::TileSmem<128>::kBytes);
-    if (st != CSWATTN_OK) return st;
   }
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  ScopedTiming tm(CSWATTN_K_DECODE, cs);
-  const bool wide = w.slot_rows > 16;
-  st = s.D == 64 ? (wide ? launch_rows_kernel<64, 2>(rp, mk, mv, cs) : launch_rows_kernel<64, 1>(rp, mk, mv, cs))
-                 : (wide ? launch_rows_kernel<128, 2>(rp, mk, mv, cs) : launch_rows_kernel<128, 1>(rp, mk, mv, cs));
-  if (st != CSWATTN_OK) return st;
-  if (w.tiles)
-    s.D == 64 ? launch_tile_kernels<64>(tp, w.plan, w.longs, mq, mk128, mv128, cs)
-              : launch_tile_kernels<128>(tp, w.plan, w.longs, mq, mk128, mv128, cs);
+  const auto launch = s.D == 64 ? launch_paged<64> : launch_paged<128>;
+  if ((st = launch(rp, tp, jp, w.tiles, mk, mv, mq, mk128, mv128, cs, true)) != CSWATTN_OK) return st;
+  {
+    ScopedTiming tm(CSWATTN_K_DECODE, cs);
+    launch(rp, tp, jp, w.tiles, mk, mv, mq, mk128, mv128, cs, false);
+  }
   return launched("paged attention launch");
 }
 
+size_t attn_paged_weigh_workspace_bytes(const cswattn_layer* layer, const cswattn_paged* paged) {
+  Shape s;
+  paged::View v;
+  if (check_paged(layer, paged, true, &s, &v) != CSWATTN_OK) return 0;
+  return carve_weigh(s, v, nullptr).bytes;
+}
+
 cswattn_status attn_paged_weigh(const cswattn_layer* layer, const cswattn_paged* paged, const void* q_out,
-                                const void* k_pages, const float* lse, float* weight, void* stream) {
+                                const void* k_pages, const float* lse, float* weight, void* workspace,
+                                size_t workspace_bytes, void* stream) {
   const NvtxRange nvtx_range("attn_paged_weigh");
   Shape s;
   paged::View v;
@@ -351,48 +407,43 @@ cswattn_status attn_paged_weigh(const cswattn_layer* layer, const cswattn_paged*
   CHECK_PTR(k_pages, 16);
   CHECK_PTR(lse, 4);
   CHECK_PTR(weight, 4);
-  const long long rows = static_cast<long long>(v.max_new) * s.g;
+  const WeighWorkspace w = carve_weigh(s, v, workspace);
+  if (w.bytes > 0) CHECK_PTR(workspace, 256);
+  if (workspace_bytes < w.bytes)
+    return fail(CSWATTN_ERR_INVALID_ARG, "weights workspace too small: %zu < %zu bytes", workspace_bytes, w.bytes);
   paged::WeighRowsParams rp;
   rp.v = v;
   rp.scale_log2 = s.scale * 1.4426950408889634f;
   rp.unit = page_unit(v.page_size, paged::kBlk);
-  rp.max_rows = rows <= 8 ? 8 : (rows <= 16 ? 16 : 32);
+  rp.max_rows = w.max_rows;
   rp.q = static_cast<const __nv_bfloat16*>(q_out);
   rp.lse = lse;
   rp.weight = weight;
   rp.wait_ns = g_wait_ns.load();
   paged::WeighTileParams tp;
+  tp.v = v;
+  tp.scale_log2 = rp.scale_log2;
+  tp.unit = page_unit(v.page_size, 128);
+  tp.tpt = 128 / s.g;
+  tp.short_rows = w.max_rows;
+  tp.plan = w.plan;
+  tp.longs = w.longs;
+  tp.lse = lse;
+  tp.weight = weight;
+  tp.part = w.part;
+  tp.wait_ns = rp.wait_ns;
   CUtensorMap mk, mq, mk128;
   if ((st = make_map(&mk, k_pages, v.n_pages, v.page_size, s.Hk, rp.unit, s.D)) != CSWATTN_OK) return st;
-  const bool tiles = rows > rp.max_rows;
-  if (tiles) {
-    tp.v = v;
-    tp.scale_log2 = rp.scale_log2;
-    tp.unit = page_unit(v.page_size, 128);
-    tp.tpt = 128 / s.g;
-    tp.short_rows = rp.max_rows;
-    tp.lse = lse;
-    tp.weight = weight;
-    tp.wait_ns = rp.wait_ns;
+  if (w.tiles) {
     if ((st = make_map_group(&mq, q_out, v.n_tokens, s.H, s.D, s.g, tp.tpt)) != CSWATTN_OK) return st;
     if ((st = make_map(&mk128, k_pages, v.n_pages, v.page_size, s.Hk, tp.unit, s.D)) != CSWATTN_OK) return st;
-    const int extra = 4 * (paged::kMaxSeqs + 1);
-    st = s.D == 64 ? set_smem(paged::weigh_tile_kernel<64>, paged::WeighTileSmem<64>::kBytes + extra)
-                   : set_smem(paged::weigh_tile_kernel<128>, paged::WeighTileSmem<128>::kBytes + extra);
-    if (st != CSWATTN_OK) return st;
   }
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  ScopedTiming tm(CSWATTN_K_DECODE, cs);
-  st = s.D == 64 ? launch_weigh_rows<64>(rp, mk, cs) : launch_weigh_rows<128>(rp, mk, cs);
-  if (st != CSWATTN_OK) return st;
-  if (tiles) {
-    const dim3 grid(paged::kWeighCtas), block(paged::kWeighThreads);
-    const size_t pre = static_cast<size_t>(4) * (v.B + 1);
-    if (s.D == 64)
-      launch_pdl(paged::weigh_tile_kernel<64>, grid, block, paged::WeighTileSmem<64>::kBytes + pre, cs, mq, mk128, tp);
-    else
-      launch_pdl(paged::weigh_tile_kernel<128>, grid, block, paged::WeighTileSmem<128>::kBytes + pre, cs, mq, mk128,
-                 tp);
+  const auto launch = s.D == 64 ? launch_weigh<64> : launch_weigh<128>;
+  if ((st = launch(rp, tp, w.tiles, mk, mq, mk128, cs, true)) != CSWATTN_OK) return st;
+  {
+    ScopedTiming tm(CSWATTN_K_DECODE, cs);
+    launch(rp, tp, w.tiles, mk, mq, mk128, cs, false);
   }
   return launched("paged weights launch");
 }

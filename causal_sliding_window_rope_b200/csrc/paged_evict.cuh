@@ -10,7 +10,7 @@
 // position, and attention over rows that are all visible does not depend on
 // their order.
 #pragma once
-#include "paged_weigh.cuh"
+#include "paged.cuh"
 
 namespace cswattn {
 namespace paged {
@@ -38,6 +38,10 @@ __device__ __forceinline__ uint32_t weight_order(float w) {
   return (u >> 31) ? ~u : (u | 0x80000000u);
 }
 
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 // Shared memory of the cluster's CTA `rank` at the place of p.
 __device__ __forceinline__ uint32_t peer_load(const void* p, int rank) {
   uint32_t a, y;

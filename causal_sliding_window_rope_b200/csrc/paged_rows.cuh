@@ -21,14 +21,13 @@
 // Units of a block that hold no visible row are not read: their box lies past
 // the pool's last page, and TMA fills it with zeros.
 #pragma once
-#include "paged.cuh"
+#include "paged_plan.cuh"
 
 namespace cswattn {
 namespace paged {
 
 constexpr int kBlk = 64;         // cached rows of a block
 constexpr int kKeyGroups = 4;    // warps that share a block, 16 rows each
-constexpr int kSMs = 148;
 constexpr int kMinBlocks = 2;    // fewest blocks worth a CTA of their own
 
 struct RowsParams {
@@ -188,9 +187,9 @@ __global__ void __launch_bounds__(32 * (kKeyGroups * MB + 1), 1)
     fence_barrier_init();
   }
   pdl_wait();
-  fill_prefix(v, pre, 16 * MB, blockIdx.x == 0);
-  const Deal deal(static_cast<long long>(pre[v.B]) * v.Hk, gridDim.x);
   const int c = blockIdx.x;
+  fill_prefix(v, pre, 16 * MB, c == 0);
+  const Deal deal(static_cast<long long>(pre[v.B]) * v.Hk, gridDim.x);
   if (c >= deal.ctas) return;
   const long long begin = deal.begin(c);
   Walk w(pre, v.B, v.Hk, begin, deal.begin(c + 1));
@@ -449,71 +448,6 @@ __global__ void __launch_bounds__(32 * (kKeyGroups * MB + 1), 1)
       p.info[static_cast<size_t>(w.b) * v.Hk + w.hk] = make_int2(2 * c + (first_seg ? 0 : 1), last - c + 1);
     }
     named_bar(1 + m, 32 * kKeyGroups);  // the staging area is free again
-  }
-}
-
-struct CombineParams {
-  View v;
-  int max_rows, slot_rows;
-  const float* part_o;
-  const float2* part_ml;
-  const int2* info;
-  __nv_bfloat16* O;
-  float* lse;
-};
-
-constexpr int kCombineThreads = 128;
-
-// CTA = (sequence, KV head), a warp per query row: the partials of a cut pair
-// joined, O = sum 2^(m_s - M) O_s / sum 2^(m_s - M) l_s.
-template <int D>
-__global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineParams p) {
-  pdl_launch_dependents();
-  pdl_wait();
-  const View& v = p.v;
-  const int b = blockIdx.x / v.Hk, hk = blockIdx.x % v.Hk, lane = lane_id();
-  Seq s;
-  int first;
-  seq_load(v, b, false, s);
-  if (visible_blocks(v, s, p.max_rows, first) == 0) return;
-  const int2 inf = p.info[blockIdx.x];
-  if (inf.y <= 1) return;
-  const int c0 = inf.x >> 1;
-  auto slot = [&](int k) { return k == 0 ? inf.x : 2 * (c0 + k); };
-  for (int r = warp_id(); r < s.n * v.g; r += kCombineThreads / 32) {
-    float M = -INFINITY;
-    for (int k = lane; k < inf.y; k += 32) M = fmaxf(M, p.part_ml[static_cast<size_t>(slot(k)) * p.slot_rows + r].x);
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float L = 0.f, a[D / 32];
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) a[i] = 0.f;
-#pragma unroll 4
-    for (int k = 0; k < inf.y; ++k) {
-      const size_t row = static_cast<size_t>(slot(k)) * p.slot_rows + r;
-      const float2 x = p.part_ml[row];
-      const float f = x.x == -INFINITY ? 0.f : ex2(x.x - M);
-      L = fmaf(x.y, f, L);
-      if constexpr (D == 128) {
-        const float4 y = *reinterpret_cast<const float4*>(p.part_o + row * D + lane * 4);
-        a[0] = fmaf(y.x, f, a[0]);
-        a[1] = fmaf(y.y, f, a[1]);
-        a[2] = fmaf(y.z, f, a[2]);
-        a[3] = fmaf(y.w, f, a[3]);
-      } else {
-        const float2 y = *reinterpret_cast<const float2*>(p.part_o + row * D + lane * 2);
-        a[0] = fmaf(y.x, f, a[0]);
-        a[1] = fmaf(y.y, f, a[1]);
-      }
-    }
-    const size_t orow = static_cast<size_t>(s.tok0 + r / v.g) * v.H + hk * v.g + r % v.g;
-    const float inv = 1.f / L;
-    if constexpr (D == 128)
-      *reinterpret_cast<uint2*>(p.O + orow * D + lane * 4) =
-          make_uint2(pack_bf16x2(a[0] * inv, a[1] * inv), pack_bf16x2(a[2] * inv, a[3] * inv));
-    else
-      *reinterpret_cast<uint32_t*>(p.O + orow * D + lane * 2) = pack_bf16x2(a[0] * inv, a[1] * inv);
-    if (lane == 0) p.lse[orow] = (M + log2f(L)) * 0.69314718055994531f;
   }
 }
 

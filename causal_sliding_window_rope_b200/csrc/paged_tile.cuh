@@ -7,9 +7,8 @@
 // tiles of one (sequence, KV head), which share the blocks of 128 cached rows
 // too. The units' blocks in a row are dealt out evenly to one CTA per SM, as
 // in the kernel of few rows (a unit is cut where a CTA's run ends; its
-// partial outputs go to the workspace and tile_combine_kernel joins them), so
+// partial outputs go to the workspace and join_kernel joins them), so
 // neither ragged chunks nor the causal edge nor a last wave leave SMs idle.
-// plan_kernel computes the deal once: where each CTA's run starts.
 //
 // Roles (12 warps), as in the dense forward:
 //   warp 0      producer: the units' Q tiles and their K and V blocks, through
@@ -31,20 +30,8 @@ namespace cswattn {
 namespace paged {
 
 constexpr int kTileThreads = 384;
-constexpr int kTileMinBlocks = 2;  // fewest blocks worth a CTA of their own
 constexpr int kTileRegLo = 80, kTileRegHi = 208;
 static_assert(128 * kTileRegLo + 256 * kTileRegHi <= kTileThreads * 168, "register budget");
-
-// Where a CTA's run starts: the k-th long sequence, KV head, unit, block of the unit.
-struct Start {
-  int k, hk, unit, t0;
-};
-
-struct Plan {
-  int ctas, n_long;
-  long long total;
-  Start start[kSMs];
-};
 
 struct TileParams {
   View v;
@@ -52,8 +39,8 @@ struct TileParams {
   int unit;        // rows of a K or V box
   int tpt;         // tokens per tile: 128 / g
   int short_rows;  // sequences with more query rows than this are this kernel's
-  const Plan* plan;
-  const int* longs;  // the long sequences, in order
+  Plan* plan;
+  int* longs;
   __nv_bfloat16* O;
   float* lse;
   float* part_o;     // (2 kSMs, 256, D)
@@ -61,167 +48,19 @@ struct TileParams {
   unsigned long long wait_ns;
 };
 
-__device__ __forceinline__ bool is_long(const View& v, const Seq& s, int short_rows) {
-  return static_cast<long long>(s.n) * v.g > short_rows;
-}
-
-// Blocks of 128 cached rows that the tokens [i0, i1) of a sequence see.
-__device__ __forceinline__ void token_blocks(const View& v, const Seq& s, int i0, int i1, int& lo, int& hi) {
-  lo = max(0, s.L + i0 - v.W + 1) >> 7;
-  hi = (s.L + i1 - 1) >> 7;
-}
-__device__ __forceinline__ int unit_blocks(const View& v, const Seq& s, int tpt, int u) {
-  int lo, hi;
-  token_blocks(v, s, u * 2 * tpt, min(s.n, (u + 1) * 2 * tpt), lo, hi);
-  return hi - lo + 1;
-}
-__device__ __forceinline__ int unit_count(const Seq& s, int tpt) { return (s.n + 2 * tpt - 1) / (2 * tpt); }
-
-constexpr int kPlanThreads = 1024;
-
-// One CTA: the blocks of every long sequence, their running sum, and the
-// start of each CTA's run (a warp per sequence, then a warp per start).
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const View v, int tpt, int short_rows, Plan* plan,
-                                                            int* longs) {
-  __shared__ long long pre[kMaxSeqs + 1];  // per long sequence: blocks of one KV head before it
-  __shared__ int s_total[33];
-  const int warp = warp_id(), lane = lane_id();
-  pdl_launch_dependents();
-  pdl_wait();
-  // The long sequences, in order.
-  int n_long = 0;
-  for (int b0 = 0; b0 < v.B; b0 += kPlanThreads) {
-    const int b = b0 + threadIdx.x;
-    bool yes = false;
-    if (b < v.B) {
-      Seq s;
-      yes = seq_load(v, b, true, s) && is_long(v, s, short_rows);
-    }
-    const uint32_t m = __ballot_sync(0xffffffffu, yes);
-    if (lane == 0) s_total[warp] = __popc(m);
-    __syncthreads();
-    int before = n_long;
-    for (int w = 0; w < warp; ++w) before += s_total[w];
-    if (yes) longs[before + __popc(m & ((1u << lane) - 1u))] = b;
-    for (int w = 0; w < 32; ++w) n_long += s_total[w];
-    __syncthreads();
-  }
-  for (int k = warp; k < n_long; k += 32) {
-    Seq s;
-    seq_load(v, longs[k], false, s);
-    long long sum = 0;
-    for (int u = lane; u < unit_count(s, tpt); u += 32) sum += unit_blocks(v, s, tpt, u);
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) pre[k + 1] = sum;
-  }
-  if (threadIdx.x == 0) pre[0] = 0;
-  __syncthreads();
-  if (warp == 0) {
-    long long run = 0;
-    for (int k0 = 0; k0 < n_long; k0 += 32) {
-      long long x = k0 + lane < n_long ? pre[k0 + lane + 1] : 0;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      if (k0 + lane < n_long) pre[k0 + lane + 1] = run + x;
-      run += __shfl_sync(0xffffffffu, x, 31);
-    }
-  }
-  __syncthreads();
-  const long long total = pre[n_long] * v.Hk;
-  const long long most = (total + kTileMinBlocks - 1) / kTileMinBlocks;
-  const int ctas = static_cast<int>(most < kSMs ? most : kSMs);
-  if (threadIdx.x == 0) {
-    plan->ctas = ctas;
-    plan->n_long = n_long;
-    plan->total = total;
-  }
-  for (int c = warp; c < ctas; c += 32) {
-    const long long at = total * c / ctas;
-    int lo = 0, hi = n_long;  // the last k with pre[k] * Hk <= at
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (pre[mid] * v.Hk <= at) lo = mid;
-      else hi = mid;
-    }
-    Seq s;
-    seq_load(v, longs[lo], false, s);
-    const long long cnt = pre[lo + 1] - pre[lo], rem = at - pre[lo] * v.Hk;
-    long long left = rem % cnt;
-    const int nu = unit_count(s, tpt);
-    for (int u0 = 0; u0 < nu; u0 += 32) {  // 32 units at a time: the one that holds block `left`
-      const int u = u0 + lane;
-      const int mine = u < nu ? unit_blocks(v, s, tpt, u) : 0;
-      int inc = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += y;
-      }
-      const bool here = u < nu && left >= inc - mine && left < inc;
-      if (here) plan->start[c] = Start{lo, static_cast<int>(rem / cnt), u, static_cast<int>(left) - (inc - mine)};
-      if (__any_sync(0xffffffffu, here)) break;
-      left -= __shfl_sync(0xffffffffu, inc, 31);
-    }
-  }
-}
-
-// A CTA's walk over its run: one segment (blocks [t0, t1) of a unit) at a time.
-struct TileWalk {
-  const TileParams& p;
-  long long left;
-  int k, hk, u, t0, t1, cnt, units, first;
-  Seq s;
-  __device__ TileWalk(const TileParams& p_, int c) : p(p_) {
-    const Start st = p.plan->start[c];
-    const long long total = p.plan->total;
-    const int ctas = p.plan->ctas;
-    left = total * (c + 1) / ctas - total * c / ctas;
-    k = st.k;
-    hk = st.hk;
-    u = st.unit;
-    t0 = st.t0;
-    load();
-    set();
-  }
-  __device__ void load() {
-    seq_load(p.v, p.longs[k], false, s);
-    units = unit_count(s, p.tpt);
-  }
-  __device__ void set() {
-    int hi;
-    token_blocks(p.v, s, u * 2 * p.tpt, min(s.n, (u + 1) * 2 * p.tpt), first, hi);
-    cnt = hi - first + 1;
-    t1 = left < cnt - t0 ? t0 + static_cast<int>(left) : cnt;
-  }
-  __device__ bool valid() const { return left > 0; }
-  __device__ void next() {
-    left -= t1 - t0;
-    t0 = 0;
-    if (left <= 0) return;
-    if (++u == units) {
-      u = 0;
-      if (++hk == p.v.Hk) {
-        hk = 0;
-        ++k;
-        load();
-      }
-    }
-    set();
-  }
-  // Blocks [lo, hi] of the segment that tile X (0 or 1) of the unit has; false if none.
+// The walk, with the blocks [lo, hi] of the segment that tile X (0 or 1) of the unit has.
+struct TileWalk : UnitWalk<TokenUnits> {
+  __device__ TileWalk(const TileParams& p, const Run& run)
+      : UnitWalk<TokenUnits>(p.v, TokenUnits{p.tpt}, run, p.longs) {}
+  __device__ bool tokens(int X) const { return (2 * u + X) * units.tpt < s.n; }
   __device__ bool tile(int X, int& lo, int& hi) const {
-    const int i0 = (2 * u + X) * p.tpt;
+    const int i0 = (2 * u + X) * units.tpt;
     if (i0 >= s.n) return false;
-    token_blocks(p.v, s, i0, min(s.n, i0 + p.tpt), lo, hi);
+    token_blocks(v, s, i0, min(s.n, i0 + units.tpt), lo, hi);
     lo = max(lo, first + t0);
     hi = min(hi, first + t1 - 1);
     return lo <= hi;
   }
-  __device__ bool tokens(int X) const { return (2 * u + X) * p.tpt < s.n; }
 };
 
 template <int D>
@@ -272,8 +111,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     *abort_flag = 0;
     fence_barrier_init();
   }
+  __shared__ Run run;
+  static_assert(kPlanSmem <= SM::kOffBar, "the plan's scratch lies where the tiles will");
   pdl_wait();
-  if (c >= p.plan->ctas) return;  // uniform over the CTA, before TMEM is taken
+  find_run(v, TokenUnits{p.tpt}, p.short_rows, gridDim.x, c, p.plan, p.longs, smem, &run);
+  if (run.left == 0) return;  // uniform over the CTA, before TMEM is taken
+  fence_proxy_async_smem();   // the scratch is written, the copies of the tiles come next
   if (warp == 1) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
@@ -298,8 +141,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       uint8_t* my_dst = smem + SM::kOffKV + my_panel * SM::kPanel + my_unit * p.unit * 128;
       int slot = 0, use = 0, issued = 0, segs = 0, q_issued = 0;
       bool ok = true;
-      for (TileWalk w(p, c); ok && w.valid(); w.next(), ++segs) {
-        const int b = p.longs[w.k];
+      for (TileWalk w(p, run); ok && w.valid(); w.next(), ++segs) {
+        const int b = w.seq();
         const int lo = max(0, w.s.L - v.W + 1), end = w.s.L + w.s.n;
         auto lookup = [&](int t) -> int {  // page of this lane's unit, or past the pool
           const int r = (w.first + t) * 128 + my_unit * p.unit;
@@ -334,14 +177,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
               mbar_expect_tx(q_full, w.tokens(1) ? 2 * bytes : bytes);
               for (int X = 0; X < 2; ++X) {
                 if (!w.tokens(X)) continue;
-                for (int pn = 0; pn < NP; ++pn) {
-                  asm volatile(
-                      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-                      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(smem + X * SM::kOp + pn * SM::kPanel)),
-                      "l"(reinterpret_cast<uint64_t>(&tmQ)), "r"(smem_u32(q_full)), "r"(64 * pn), "r"(w.hk * v.g),
-                      "r"(w.s.tok0 + (2 * w.u + X) * p.tpt)
-                      : "memory");
-                }
+                for (int pn = 0; pn < NP; ++pn)
+                  tma_load_3d(&tmQ, q_full, smem + X * SM::kOp + pn * SM::kPanel, 64 * pn, w.hk * v.g,
+                              w.s.tok0 + (2 * w.u + X) * p.tpt);
               }
             }
             ++q_issued;
@@ -367,7 +205,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         int base = 0, segs = 0;  // blocks of earlier segments; segments
         int np[2] = {0, 0};      // P tiles taken, per tile
         bool ok = true;
-        for (TileWalk w(p, c); ok && w.valid(); w.next(), ++segs) {
+        for (TileWalk w(p, run); ok && w.valid(); w.next(), ++segs) {
           const int lo = w.first + w.t0, hi = w.first + w.t1 - 1;
           int lo_t[2], hi_t[2];
           bool on[2];
@@ -451,7 +289,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const float c2 = p.scale_log2;
     int base = 0, ns = 0, no = 0;  // blocks of earlier segments; S and O tiles taken
     bool ok = true, first_seg = true;
-    for (TileWalk w(p, c); ok && w.valid(); w.next(), first_seg = false) {
+    for (TileWalk w(p, run); ok && w.valid(); w.next(), first_seg = false) {
       int lo_t, hi_t;
       const bool on = w.tile(X, lo_t, hi_t);
       const int seg_lo = w.first + w.t0, end = w.s.L + w.s.n, lo_seq = max(0, w.s.L - v.W + 1);
@@ -580,7 +418,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       base += w.t1 - w.t0;
       // The row's output, or its share of it.
-      const bool whole = w.t0 == 0 && w.t1 == w.cnt;
+      const bool whole = w.whole();
       const size_t orow = live ? static_cast<size_t>(w.s.tok0 + i) * v.H + w.hk * v.g + r % v.g : 0;
       const size_t prow = static_cast<size_t>(2 * c + (first_seg ? 0 : 1)) * 256 + X * 128 + r;
       if (live) {
@@ -625,41 +463,45 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   }
 }
 
-constexpr int kTileCombineRows = 8;  // rows (warps) of a CTA
+struct JoinParams {
+  View v;
+  // pairs that rows_kernel cut
+  int max_rows;       // query rows of a slot
+  const float* part_o;
+  const float2* part_ml;
+  const int2* info;
+  // units that tile_kernel cut
+  int tpt;
+  const Plan* plan;
+  const int* longs;
+  const float* tile_o;
+  const float2* tile_ml;
+  __nv_bfloat16* O;
+  float* lse;
+};
 
-// CTA = (boundary between two CTAs' runs, 8 rows): the unit cut there, if the
-// boundary is its first, from the shares of all CTAs that had a part of it.
-template <int D>
-__global__ void __launch_bounds__(32 * kTileCombineRows) tile_combine_kernel(const __grid_constant__ TileParams p) {
-  pdl_launch_dependents();
-  pdl_wait();
-  const int c = blockIdx.x + 1, lane = lane_id();
-  const Plan* plan = p.plan;
-  if (c >= plan->ctas) return;
-  const View& v = p.v;
-  const Start st = plan->start[c], before = plan->start[c - 1];
-  auto same = [&](const Start& a) { return a.k == st.k && a.hk == st.hk && a.unit == st.unit; };
-  if (st.t0 == 0 || (same(before) && before.t0 > 0)) return;
-  int last = c;
-  while (last + 1 < plan->ctas && same(plan->start[last + 1])) ++last;
-  const int slot0 = 2 * (c - 1) + (same(before) ? 0 : 1);
-  Seq s;
-  seq_load(v, p.longs[st.k], false, s);
-  const int row = blockIdx.y * kTileCombineRows + warp_id();  // of the unit's two tiles
-  const int r = row & 127, i = (2 * st.unit + (row >> 7)) * p.tpt + r / v.g;
-  if (r >= p.tpt * v.g || i >= s.n) return;
-  auto at = [&](int k) { return static_cast<size_t>(k < c ? slot0 : 2 * k) * 256 + row; };
+constexpr int kJoinWarps = 8;  // output rows of a CTA
+
+// One output row by one warp, from n partials (maximum, sum, output):
+// O = sum 2^(m - M) O_i / sum 2^(m - M) l_i; at(i) is the place of the i-th.
+template <int D, class At>
+__device__ __forceinline__ void join_row(const float* part_o, const float2* part_ml, int n, const At& at,
+                                         __nv_bfloat16* O, float* lse) {
+  const int lane = lane_id();
   float M = -INFINITY;
-  for (int k = c - 1; k <= last; ++k) M = fmaxf(M, p.part_ml[at(k)].x);
+  for (int k = lane; k < n; k += 32) M = fmaxf(M, part_ml[at(k)].x);
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   float L = 0.f, a[D / 32];
 #pragma unroll
   for (int e = 0; e < D / 32; ++e) a[e] = 0.f;
-  for (int k = c - 1; k <= last; ++k) {
-    const float2 x = p.part_ml[at(k)];
+#pragma unroll 4
+  for (int k = 0; k < n; ++k) {
+    const float2 x = part_ml[at(k)];
     if (x.x == -INFINITY) continue;  // no key of this share: its output may not be written
     const float f = ex2(x.x - M);
     L = fmaf(x.y, f, L);
-    const float* src = p.part_o + at(k) * D + lane * (D / 32);
+    const float* src = part_o + at(k) * D + lane * (D / 32);
 #pragma unroll
     for (int e = 0; e < D / 32; e += 2) {
       const float2 y = *reinterpret_cast<const float2*>(src + e);
@@ -667,12 +509,48 @@ __global__ void __launch_bounds__(32 * kTileCombineRows) tile_combine_kernel(con
       a[e + 1] = fmaf(y.y, f, a[e + 1]);
     }
   }
-  const size_t orow = static_cast<size_t>(s.tok0 + i) * v.H + st.hk * v.g + r % v.g;
   const float inv = 1.f / L;
 #pragma unroll
   for (int e = 0; e < D / 32; e += 2)
-    *reinterpret_cast<uint32_t*>(p.O + orow * D + lane * (D / 32) + e) = pack_bf16x2(a[e] * inv, a[e + 1] * inv);
-  if (lane == 0) p.lse[orow] = (M + log2f(L)) * 0.69314718055994531f;
+    *reinterpret_cast<uint32_t*>(O + lane * (D / 32) + e) = pack_bf16x2(a[e] * inv, a[e + 1] * inv);
+  if (lane == 0) *lse = (M + log2f(L)) * 0.69314718055994531f;
+}
+
+// CTAs [0, B Hk): a (sequence, KV head) pair that rows_kernel cut. The CTAs
+// behind them: a boundary between two CTAs' runs of tile_kernel and 8 of the
+// 256 rows of the unit cut there.
+template <int D>
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const JoinParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const View& v = p.v;
+  Seq s;
+  auto out_row = [&](int hk, int i, int h) { return static_cast<size_t>(s.tok0 + i) * v.H + hk * v.g + h; };
+  const int pairs = v.B * v.Hk;
+  if (static_cast<int>(blockIdx.x) < pairs) {
+    const int b = blockIdx.x / v.Hk, hk = blockIdx.x % v.Hk;
+    const int2 inf = p.info[blockIdx.x];  // unspecified for a sequence that is not rows_kernel's
+    int first;
+    seq_load(v, b, false, s);
+    if (visible_blocks(v, s, p.max_rows, first) == 0 || inf.y <= 1) return;
+    for (int r = warp_id(); r < s.n * v.g; r += kJoinWarps) {
+      const size_t row = out_row(hk, r / v.g, r % v.g);
+      join_row<D>(p.part_o, p.part_ml, inf.y,
+                  [&](int k) { return static_cast<size_t>(k == 0 ? inf.x : 2 * ((inf.x >> 1) + k)) * p.max_rows + r; },
+                  p.O + row * D, p.lse + row);
+    }
+    return;
+  }
+  const int x = blockIdx.x - pairs;
+  Cut cut;
+  if (!cut.find(p.plan, x / (256 / kJoinWarps) + 1)) return;
+  seq_load(v, p.longs[cut.st.k], false, s);
+  const int row = x % (256 / kJoinWarps) * kJoinWarps + warp_id();  // of the unit's two tiles
+  const int r = row & 127, i = (2 * cut.st.unit + (row >> 7)) * p.tpt + r / v.g;
+  if (r >= p.tpt * v.g || i >= s.n) return;
+  const size_t o = out_row(cut.st.hk, i, r % v.g);
+  join_row<D>(p.tile_o, p.tile_ml, cut.last - cut.c + 2,
+              [&](int k) { return static_cast<size_t>(cut.slot(cut.c - 1 + k)) * 256 + row; }, p.O + o * D, p.lse + o);
 }
 
 }  // namespace paged

@@ -32,6 +32,8 @@ struct WeighRowsParams {
   unsigned long long wait_ns;
 };
 
+constexpr int kWeighRuns = 2 * kSMs;  // CTAs of weigh_tile_kernel, two per SM
+
 template <int D>
 struct WeighRowsSmem {
   static constexpr int kPanel = kBlk * 128;
@@ -213,81 +215,57 @@ struct WeighTileParams {
   View v;
   float scale_log2;
   int unit, tpt, short_rows;
+  Plan* plan;
+  int* longs;
   const float* lse;
   float* weight;
+  float* part;  // (2 kWeighRuns, 128): sums of cut units
   unsigned long long wait_ns;
 };
 
-constexpr int kWeighThreads = 320;  // producer, MMA issuer, 8 warps of sums
-constexpr int kWeighCluster = 4;    // CTAs that may share a unit's query tiles
-constexpr int kWeighCtas = 2 * kSMs;  // two per SM: one's products and copies under the other's sums
-constexpr int kWeighWhole = 6;      // units per CTA from which each takes whole ones
+constexpr int kWeighThreads = 320;  // producer, MMA issuer (and the query rows' terms), 8 warps of sums
 
 template <int D>
 struct WeighTileSmem {
   static constexpr int kPanel = 128 * 128;
   static constexpr int kOp = (D / 64) * kPanel;
-  static constexpr int kOffQ = kOp;                 // 2 slots
-  static constexpr int kOffLse = 3 * kOp;           // [2][128] float
-  static constexpr int kOffSum = kOffLse + 1024;    // [2][kWeighCluster - 1][128] float: the other CTAs' sums
-  static constexpr int kOffHalf = kOffSum + 2 * (kWeighCluster - 1) * 512;  // [128] float: the second half's sums
-  static constexpr int kOffBar = kOffHalf + 512;
-  static constexpr int kOffPre = kOffBar + 8 * 18;  // int [B + 1]
-  static constexpr int kBytes = kOffPre + 1024;     // and 4 (B + 1) more; two CTAs fit an SM
-  static_assert(kBytes + 4 * (kMaxSeqs + 1) <= 232448, "shared memory per block");
+  static constexpr int kOffQ = kOp;                  // 2 slots
+  static constexpr int kOffTerm = 3 * kOp;           // [2][128] float
+  static constexpr int kOffHalf = kOffTerm + 1024;   // [2][128] float: the second half's sums
+  static constexpr int kOffBar = kOffHalf + 1024;
+  static constexpr int kBytes = kOffBar + 8 * 20 + 1024;
+  static_assert(2 * (kBytes + 1024) <= 233472, "two blocks per SM");
 };
 
-// Shared memory of another CTA of the cluster: address, store, arrival; and
-// the wait that sees what was stored before the arrivals.
-__device__ __forceinline__ uint32_t cluster_addr(const void* p, int rank) {
-  uint32_t a;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-  return a;
-}
-__device__ __forceinline__ void cluster_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ bool cluster_wait(uint64_t* bar, uint32_t parity, const WaitCtx& w) {
-  if (!mbar_wait(bar, parity, w)) return false;
-  asm volatile("fence.acq_rel.cluster;" ::: "memory");
-  return true;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// CTA (or cluster of kWeighCluster) = one 128-row tile of cached rows after
-// another; the query tiles that see it stream past. With a cluster, CTA `rank`
-// takes every kWeighCluster-th query tile; the others write their sums into
-// rank 0's shared memory (two buffers, handed back by an arrival), which adds
-// them in the order of the ranks. All threads meet at the cluster's barrier
-// once at the start (barriers set up) and once at the end (no CTA leaves
-// while another may still reach its shared memory); no path skips either.
+// The deal's units are tiles of 128 cached rows, their blocks the query tiles
+// that see them. K stays, the query tiles stream past: S^T = K Q^T in one of
+// two TMEM buffers, and two threads per cached row add up 64 columns each.
+// Two CTAs per SM, so that one's products, copies and ends of units run under
+// the other's sums. The sums of a cut unit go to `part`.
 template <int D>
-__global__ void __launch_bounds__(kWeighThreads, 2) __cluster_dims__(kWeighCluster, 1, 1)
+__global__ void __launch_bounds__(kWeighThreads, 2)
     weigh_tile_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ WeighTileParams p) {
   using SM = WeighTileSmem<D>;
   constexpr int NP = D / 64;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_align1024(smem_raw);
-  float* s_lse = reinterpret_cast<float*>(smem + SM::kOffLse);
-  float* s_sum = reinterpret_cast<float*>(smem + SM::kOffSum);  // [2][kWeighCluster - 1][128]
+  float* s_term = reinterpret_cast<float*>(smem + SM::kOffTerm);
+  float* s_half = reinterpret_cast<float*>(smem + SM::kOffHalf);
   uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + SM::kOffBar);
   uint64_t* k_empty = k_full + 1;
-  uint64_t* q_full = k_full + 2;    // [2]
-  uint64_t* q_empty = k_full + 4;   // [2]
-  uint64_t* s_full = k_full + 6;    // [2] S^T buffers
-  uint64_t* s_empty = k_full + 8;   // [2] (256 arrivals)
-  uint64_t* mma_done = k_full + 10;
-  uint64_t* sum_full = k_full + 11;  // [2] rank 0: the others' sums have come
-  uint64_t* sum_free = k_full + 13;  // [2] the others: rank 0 has read the buffer
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(k_full + 15);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(k_full + 16);
-  int* pre = reinterpret_cast<int*>(smem + SM::kOffPre);
+  uint64_t* q_full = k_full + 2;     // [2]
+  uint64_t* q_empty = k_full + 4;    // [2]
+  uint64_t* s_full = k_full + 6;     // [2] S^T buffers
+  uint64_t* s_empty = k_full + 8;    // [2] read by all sums (256 arrivals); the terms' buffer with it
+  uint64_t* t_full = k_full + 10;    // [2] terms written (32 arrivals)
+  uint64_t* h_full = k_full + 12;    // [2] the second half's sums written (128 arrivals)
+  uint64_t* h_empty = k_full + 14;   // [2] ... and read (128 arrivals)
+  uint64_t* mma_done = k_full + 16;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(k_full + 17);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(k_full + 18);
   const View& v = p.v;
-  const int warp = warp_id(), lane = lane_id();
+  const int warp = warp_id(), lane = lane_id(), c = blockIdx.x;
   pdl_launch_dependents();
   if (threadIdx.x == 0) {
     mbar_init(k_full, 1);
@@ -297,83 +275,30 @@ __global__ void __launch_bounds__(kWeighThreads, 2) __cluster_dims__(kWeighClust
       mbar_init(&q_empty[i], 1);
       mbar_init(&s_full[i], 1);
       mbar_init(&s_empty[i], 256);
-      mbar_init(&sum_full[i], 128 * (kWeighCluster - 1));
-      mbar_init(&sum_free[i], 1);
+      mbar_init(&t_full[i], 32);
+      mbar_init(&h_full[i], 128);
+      mbar_init(&h_empty[i], 128);
     }
     mbar_init(mma_done, 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
+  __shared__ Run run;
+  static_assert(kPlanSmem <= SM::kOffTerm, "the plan's scratch lies where the tiles will");
+  pdl_wait();
+  find_run(v, RowUnits{p.tpt}, p.short_rows, gridDim.x, c, p.plan, p.longs, smem, &run);
+  if (run.left == 0) return;  // uniform over the CTA, before TMEM is taken
+  fence_proxy_async_smem();   // the scratch is written, the copies of the tiles come next
   if (warp == 1) {
     tmem_alloc(tmem_slot, 256);
     tmem_relinquish();
   }
-  pdl_wait();
-  // Tiles of cached rows of each long sequence, and their running sum.
-  for (int b = threadIdx.x; b < v.B; b += kWeighThreads) {
-    Seq s;
-    seq_load(v, b, blockIdx.x == 0, s);
-    int lo, hi, n = 0;
-    if (is_long(v, s, p.short_rows)) {
-      token_blocks(v, s, 0, s.n, lo, hi);
-      n = hi - lo + 1;
-    }
-    pre[b + 1] = n;
-  }
-  if (threadIdx.x == 0) pre[0] = 0;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 0) {
-    int run = 0;
-    for (int b0 = 0; b0 < v.B; b0 += 32) {
-      const int b = b0 + lane;
-      int x = b < v.B ? pre[b + 1] : 0;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      if (b < v.B) pre[b + 1] = run + x;
-      run += __shfl_sync(0xffffffffu, x, 31);
-    }
-  }
-  __syncthreads();
-  cluster_sync();
   const uint32_t tmem = *tmem_slot;
   const WaitCtx wc{abort_flag, p.wait_ns};
-  const long long units = static_cast<long long>(pre[v.B]) * v.Hk;
-  const bool shared = units < static_cast<long long>(kWeighWhole) * gridDim.x;
-  const int rank = shared ? blockIdx.x % kWeighCluster : 0, ranks = shared ? kWeighCluster : 1;
-  const long long first_unit = shared ? blockIdx.x / kWeighCluster : blockIdx.x;
-  const long long stride = shared ? gridDim.x / kWeighCluster : gridDim.x;
-
-  // Unit u: sequence b, KV head hk, tile of cached rows [k0, k0 + 128); this
-  // CTA's query tiles are q0, q0 + ranks, ... <= q1 (of tpt tokens each).
-  struct Unit {
-    int b, hk, k0, q0, q1;
-    Seq s;
-  };
-  auto unit_at = [&](long long u) -> Unit {
-    int lo = 0, hi = v.B;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (static_cast<long long>(pre[mid]) * v.Hk <= u) lo = mid;
-      else hi = mid;
-    }
-    Unit x;
-    x.b = lo;
-    seq_load(v, lo, false, x.s);
-    const int rem = static_cast<int>(u - static_cast<long long>(pre[lo]) * v.Hk), cnt = pre[lo + 1] - pre[lo];
-    x.hk = rem / cnt;
-    x.k0 = ((max(0, x.s.L - v.W + 1) >> 7) + rem % cnt) * 128;
-    // tokens i with k <= L + i and L + i - W < k for some k of the tile
-    const int i_lo = max(0, x.k0 - x.s.L);
-    const long long i_hi = min(static_cast<long long>(x.s.n) - 1, static_cast<long long>(x.k0) + 127 - x.s.L + v.W - 1);
-    x.q0 = i_lo / p.tpt + rank;
-    x.q1 = i_hi < i_lo ? -1 : static_cast<int>(i_hi) / p.tpt;
-    return x;
-  };
+  UnitWalk<RowUnits> w(v, RowUnits{p.tpt}, run, p.longs);
   bool ok = true;
 
   if (warp == 0) {
@@ -385,14 +310,12 @@ __global__ void __launch_bounds__(kWeighThreads, 2) __cluster_dims__(kWeighClust
     const int boxes = (128 / p.unit) * NP;
     const int my_unit = lane / NP, my_panel = lane % NP;
     int nk = 0, nq = 0;
-    for (long long u = first_unit; ok && u < units; u += stride) {
-      const Unit x = unit_at(u);
-      if (x.q0 > x.q1) continue;
-      const int lo = max(0, x.s.L - v.W + 1), end = x.s.L + x.s.n;
-      int page = v.n_pages;
-      const int r = x.k0 + my_unit * p.unit;
+    for (; ok && w.valid(); w.next()) {
+      const int lo = max(0, w.s.L - v.W + 1), end = w.s.L + w.s.n;
+      const int r = w.units.first_row(v, w.s, w.u) + my_unit * p.unit;
+      int page = v.n_pages;  // past the pool: zeros
       if (lane < boxes && r < end && r + p.unit > lo) {
-        page = page_at(v, x.b, r / v.page_size);
+        page = page_at(v, w.seq(), r / v.page_size);
         if (page < 0) page = v.n_pages;
       }
       if (nk > 0) ok = __all_sync(0xffffffffu, mbar_wait(k_empty, (nk - 1) & 1, wc));
@@ -400,22 +323,18 @@ __global__ void __launch_bounds__(kWeighThreads, 2) __cluster_dims__(kWeighClust
       if (lane == 0) mbar_expect_tx(k_full, SM::kOp);
       __syncwarp();
       if (lane < boxes)
-        tma_load_4d(&tmK, k_full, smem + my_panel * SM::kPanel + my_unit * p.unit * 128, 64 * my_panel, x.hk,
+        tma_load_4d(&tmK, k_full, smem + my_panel * SM::kPanel + my_unit * p.unit * 128, 64 * my_panel, w.hk,
                     r % v.page_size, page);
       ++nk;
       if (lane == 0) {
-        for (int q = x.q0; ok && q <= x.q1; q += ranks, ++nq) {
+        for (int t = w.t0; ok && t < w.t1; ++t, ++nq) {
           const int slot = nq & 1;
           if (nq > 1) ok = mbar_wait(&q_empty[slot], ((nq >> 1) - 1) & 1, wc);
           if (!ok) break;
           mbar_expect_tx(&q_full[slot], p.tpt * v.g * 128 * NP);
           for (int pn = 0; pn < NP; ++pn)
-            asm volatile(
-                "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-                " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(smem + SM::kOffQ + slot * SM::kOp + pn * SM::kPanel)),
-                "l"(reinterpret_cast<uint64_t>(&tmQ)), "r"(smem_u32(&q_full[slot])), "r"(64 * pn), "r"(x.hk * v.g),
-                "r"(x.s.tok0 + q * p.tpt)
-                : "memory");
+            tma_load_3d(&tmQ, &q_full[slot], smem + SM::kOffQ + slot * SM::kOp + pn * SM::kPanel, 64 * pn, w.hk * v.g,
+                        w.s.tok0 + (w.first + t) * p.tpt);
         }
       }
       ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
@@ -425,90 +344,105 @@ __global__ void __launch_bounds__(kWeighThreads, 2) __cluster_dims__(kWeighClust
       for (int i = 0; i < 2 && i < nq; ++i) drain_wait(&q_full[i], ((nq - 1 - i) >> 1) & 1);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      // -------------------------------------------------- S^T = K Q^T
-      constexpr uint32_t idS = idesc_bf16(128, 128, 0, 0);
-      const uint64_t dK = sdesc_sw128(smem_u32(smem), 16, 1024);
-      const uint64_t dQ = sdesc_sw128(smem_u32(smem + SM::kOffQ), 16, 1024);
-      int nk = 0, nq = 0;
-      for (long long u = first_unit; ok && u < units; u += stride) {
-        const Unit x = unit_at(u);
-        if (x.q0 > x.q1) continue;
-        ok = mbar_wait(k_full, nk & 1, wc);
-        ++nk;
-        for (int q = x.q0; ok && q <= x.q1; q += ranks, ++nq) {
-          const int buf = nq & 1;
-          ok = mbar_wait(&q_full[buf], (nq >> 1) & 1, wc) &&
-               (nq < 2 || mbar_wait(&s_empty[buf], ((nq >> 1) - 1) & 1, wc));
-          if (!ok) break;
-          tc_fence_after();
+    // ---------------------------------------------------- S^T = K Q^T, and -lse log2(e) of the query rows
+    constexpr uint32_t idS = idesc_bf16(128, 128, 0, 0);
+    const uint64_t dK = sdesc_sw128(smem_u32(smem), 16, 1024);
+    const uint64_t dQ = sdesc_sw128(smem_u32(smem + SM::kOffQ), 16, 1024);
+    int nk = 0, nq = 0;
+    for (; ok && w.valid(); w.next()) {
+      for (int t = w.t0; t < w.t1; ++t, ++nq) {
+        const int buf = nq & 1, i0 = (w.first + t) * p.tpt;
+        float term[4];
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint64_t off = static_cast<uint64_t>(((kk >> 2) * SM::kPanel + (kk & 3) * 32) >> 4);
-            mma_ss(tmem + buf * 128u, dK + off, dQ + static_cast<uint64_t>((buf * SM::kOp) >> 4) + off, idS,
-                   kk > 0 ? 1u : 0u);
-          }
-          mma_commit(&q_empty[buf]);
-          mma_commit(&s_full[buf]);
+        for (int e = 0; e < 4; ++e) {
+          const int r = lane + 32 * e, i = i0 + r / v.g;
+          term[e] = r < p.tpt * v.g && i < w.s.n
+                        ? p.lse[static_cast<size_t>(w.s.tok0 + i) * v.H + w.hk * v.g + r % v.g] * -1.4426950408889634f
+                        : 0.f;
         }
-        if (ok) mma_commit(k_empty);
+        if (nq > 1) ok = __all_sync(0xffffffffu, mbar_wait(&s_empty[buf], ((nq >> 1) - 1) & 1, wc));
+        if (!ok) break;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s_term[buf * 128 + lane + 32 * e] = term[e];
+        mbar_arrive(&t_full[buf]);
+        if (lane == 0) {
+          ok = (t > w.t0 || mbar_wait(k_full, nk & 1, wc)) && mbar_wait(&q_full[buf], (nq >> 1) & 1, wc);
+          if (ok) {
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint64_t off = static_cast<uint64_t>(((kk >> 2) * SM::kPanel + (kk & 3) * 32) >> 4);
+              mma_ss(tmem + buf * 128u, dK + off, dQ + static_cast<uint64_t>((buf * SM::kOp) >> 4) + off, idS,
+                     kk > 0 ? 1u : 0u);
+            }
+            mma_commit(&q_empty[buf]);
+            mma_commit(&s_full[buf]);
+            if (t + 1 == w.t1) mma_commit(k_empty);
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        if (!ok) break;
       }
+      ++nk;
+    }
+    if (lane == 0) {
       mma_commit(mma_done);
       drain_wait(mma_done, 0);
     }
+    __syncwarp();
   } else {
     // ---------------------------------------------------- sums: two threads per cached row
     // Warps 2-5 take columns 0-63 of each tile, warps 6-9 columns 64-127.
     const int quad = warp & 3, r = quad * 32 + lane, half = warp >= 6 ? 1 : 0;
-    float* s_half = reinterpret_cast<float*>(smem + SM::kOffHalf);
-    const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t tS = tmem + (static_cast<uint32_t>(quad * 32) << 16) + 64u * half;
     const float c2 = p.scale_log2;
     int nq = 0, nu = 0;
-    for (long long u = first_unit; ok && u < units; u += stride, ++nu) {
-      const Unit x = unit_at(u);
-      const int key = x.k0 + r, end = x.s.L + x.s.n;
-      const bool mine = key < end && key > x.s.L - v.W;
-      float total = 0.f;
-      // Row r of query tile q: its log-sum-exp in log2 units, negated.
-      auto row_term = [&](int q) -> float {
-        const int i = q * p.tpt + r / v.g;
-        return q <= x.q1 && r < p.tpt * v.g && i < x.s.n
-                   ? p.lse[static_cast<size_t>(x.s.tok0 + i) * v.H + x.hk * v.g + r % v.g] * -1.4426950408889634f
-                   : 0.f;
-      };
-      float term = half == 0 ? row_term(x.q0) : 0.f;
-      for (int q = x.q0; ok && q <= x.q1; q += ranks, ++nq) {
-        const int buf = nq & 1, i0 = q * p.tpt;
-        if (half == 0) {
-          s_lse[buf * 128 + r] = term;
-          term = row_term(q + ranks);  // the next tile's, under this one's sums
+    for (; ok && w.valid(); w.next(), ++nu) {
+      const int key = w.units.first_row(v, w.s, w.u) + r, end = w.s.L + w.s.n;
+      const bool whole = w.whole();
+      // The row this thread updates: its place and old weight, under the first products.
+      float* place = nullptr;
+      float old = 0.f;
+      if (half == 0) {
+        if (!whole) {
+          place = p.part + static_cast<size_t>(2 * c + (nu == 0 ? 0 : 1)) * 128 + r;
+        } else if (key < end && key > w.s.L - v.W) {
+          const int page = page_at(v, w.seq(), key / v.page_size);
+          if (page >= 0) {
+            place = p.weight + term_index(v, page, key % v.page_size, w.hk);
+            old = *place;
+          }
         }
-        ok = named_bar_and(1, 256, mbar_wait(&s_full[buf], (nq >> 1) & 1, wc));
+      }
+      float total = 0.f;
+      for (int t = w.t0; t < w.t1; ++t, ++nq) {
+        const int buf = nq & 1, i0 = (w.first + t) * p.tpt;
+        // Columns [a, b] of this half are the query rows that see this cached
+        // row: key - L <= token < key - L + W.
+        // (rows and windows are below 2^20, g at most 128: 32 bits hold the products)
+        const int past = key - w.s.L - i0;
+        const int a = max(0, past * v.g) - 64 * half;
+        const int b = min(min(p.tpt, w.s.n - i0) * v.g, (past + v.W) * v.g) - 1 - 64 * half;
+        ok = __all_sync(0xffffffffu, mbar_wait(&t_full[buf], (nq >> 1) & 1, wc) &&
+                                         mbar_wait(&s_full[buf], (nq >> 1) & 1, wc));
         if (!ok) break;
         tc_fence_after();
-        // Columns [a, b] are the query rows that see this cached row:
-        // key - L <= token < key - L + W.
-        const int cols = min(p.tpt, x.s.n - i0) * v.g;
-        const long long lo_col = (static_cast<long long>(key) - x.s.L - i0) * v.g;
-        const long long hi_col = (static_cast<long long>(key) - x.s.L + v.W - i0) * v.g - 1;
-        const int a = static_cast<int>(max(0ll, lo_col));
-        const int b = static_cast<int>(min(static_cast<long long>(cols) - 1, hi_col));
         float part[4] = {0.f, 0.f, 0.f, 0.f};
+        uint32_t sv[2][32];
+        tmem_ld32(tS + buf * 128, sv[0]);
+        tmem_ld32(tS + buf * 128 + 32, sv[1]);
+        tmem_ld_wait();
 #pragma unroll
-        for (int h2 = 0; h2 < 2; ++h2) {
-          const int h = 2 * half + h2;
+        for (int h = 0; h < 2; ++h) {
           if (!__any_sync(0xffffffffu, a <= 32 * h + 31 && b >= 32 * h)) continue;  // nobody sees these
-          uint32_t sv[32];
-          tmem_ld32(tmem + lane_off + buf * 128 + h * 32, sv);
-          tmem_ld_wait();
           const bool all = __all_sync(0xffffffffu, a <= 32 * h && b >= 32 * h + 31);
 #pragma unroll
           for (int e4 = 0; e4 < 8; ++e4) {
-            const float4 l4 = *reinterpret_cast<const float4*>(&s_lse[buf * 128 + h * 32 + e4 * 4]);
-            const float x0 = ex2(fmaf(__uint_as_float(sv[4 * e4]), c2, l4.x));
-            const float x1 = ex2(fmaf(__uint_as_float(sv[4 * e4 + 1]), c2, l4.y));
-            const float x2 = ex2(fmaf(__uint_as_float(sv[4 * e4 + 2]), c2, l4.z));
-            const float x3 = ex2(fmaf(__uint_as_float(sv[4 * e4 + 3]), c2, l4.w));
+            const float4 l4 = *reinterpret_cast<const float4*>(&s_term[buf * 128 + 64 * half + h * 32 + e4 * 4]);
+            const float x0 = ex2(fmaf(__uint_as_float(sv[h][4 * e4]), c2, l4.x));
+            const float x1 = ex2(fmaf(__uint_as_float(sv[h][4 * e4 + 1]), c2, l4.y));
+            const float x2 = ex2(fmaf(__uint_as_float(sv[h][4 * e4 + 2]), c2, l4.z));
+            const float x3 = ex2(fmaf(__uint_as_float(sv[h][4 * e4 + 3]), c2, l4.w));
             if (all) {
               part[0] += x0;
               part[1] += x1;
@@ -528,45 +462,48 @@ __global__ void __launch_bounds__(kWeighThreads, 2) __cluster_dims__(kWeighClust
         mbar_arrive(&s_empty[buf]);
       }
       if (!ok) break;
-      // The two halves of a row meet; warps 2-5 go on with its sum.
-      if (half == 1) s_half[r] = total;
-      named_bar(1, 256);
-      if (half == 0) {
-        total += s_half[r];
-        const int buf = nu & 1;
-        float* slot = s_sum + buf * (kWeighCluster - 1) * 128 + r;
-        if (shared && rank > 0) {
-          ok = named_bar_and(2, 128, nu < 2 || mbar_wait(&sum_free[buf], ((nu >> 1) - 1) & 1, wc));
-          if (ok) {
-            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr(slot + (rank - 1) * 128, 0)), "f"(total)
-                         : "memory");
-            cluster_arrive(cluster_addr(&sum_full[buf], 0));
-          }
-        } else if (shared) {
-          ok = named_bar_and(2, 128, cluster_wait(&sum_full[buf], (nu >> 1) & 1, wc));
-          if (ok) {
-#pragma unroll
-            for (int k = 0; k < kWeighCluster - 1; ++k) total += slot[k * 128];
-            named_bar(2, 128);  // every thread has read the buffer
-            if (r > 0 && r < kWeighCluster) cluster_arrive(cluster_addr(&sum_free[buf], r));
-          }
-        }
-        if (ok && rank == 0 && mine) {
-          const int page = page_at(v, x.b, key / v.page_size);
-          if (page >= 0) p.weight[term_index(v, page, key % v.page_size, x.hk)] += total;
-        }
+      // The second half hands its sum over; the first adds and writes.
+      const int hb = nu & 1;
+      if (half == 1) {
+        ok = __all_sync(0xffffffffu, nu < 2 || mbar_wait(&h_empty[hb], ((nu >> 1) - 1) & 1, wc));
+        if (!ok) break;
+        s_half[hb * 128 + r] = total;
+        mbar_arrive(&h_full[hb]);
+      } else {
+        ok = __all_sync(0xffffffffu, mbar_wait(&h_full[hb], (nu >> 1) & 1, wc));
+        if (!ok) break;
+        total += s_half[hb * 128 + r];
+        mbar_arrive(&h_empty[hb]);
+        if (place) *place = whole ? old + total : total;
       }
-      ok = named_bar_and(1, 256, ok);  // all leave together when a wait ran out
     }
   }
-  __syncwarp();
-  cluster_sync();
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 256);
   }
+}
+
+// CTA = a boundary between two CTAs' runs: the unit cut there gets its shares
+// in the order of the CTAs that have them.
+__global__ void __launch_bounds__(128) weigh_join_kernel(const __grid_constant__ WeighTileParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  Cut cut;
+  if (!cut.find(p.plan, blockIdx.x + 1)) return;
+  const View& v = p.v;
+  const int b = p.longs[cut.st.k];
+  Seq s;
+  seq_load(v, b, false, s);
+  const int key = RowUnits{p.tpt}.first_row(v, s, cut.st.unit) + threadIdx.x;
+  if (key >= s.L + s.n || key <= s.L - v.W) return;
+  const int page = page_at(v, b, key / v.page_size);
+  if (page < 0) return;
+  float total = 0.f;
+  for (int k = cut.c - 1; k <= cut.last; ++k) total += p.part[static_cast<size_t>(cut.slot(k)) * 128 + threadIdx.x];
+  p.weight[term_index(v, page, key % v.page_size, cut.st.hk)] += total;
 }
 
 }  // namespace paged

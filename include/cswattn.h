@@ -384,9 +384,16 @@ cswattn_status attn_paged(const cswattn_layer* layer, const cswattn_paged* paged
  *   heads h of the group of exp(softmax_scale * q_out[i,h] . k[row] - lse[i,h])
  * with attn_paged's lse. The sum's order is fixed: the same call on the same
  * data gives the same bits. Pages must not be shared between sequences (each
- * row of `weight` is updated without atomics). */
+ * row of `weight` is updated without atomics). workspace: as for attn_paged,
+ * attn_paged_weigh_workspace_bytes of it; NULL where that is 0 (max_new times
+ * the heads of a group at most 32). */
 cswattn_status attn_paged_weigh(const cswattn_layer* layer, const cswattn_paged* paged, const void* q_out,
-                                const void* k_pages, const float* lse, float* weight, void* stream);
+                                const void* k_pages, const float* lse, float* weight, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+/* Bytes of device scratch attn_paged_weigh needs (0 for a call of few query
+ * rows, and for an invalid or unsupported layer or batch). */
+size_t attn_paged_weigh_workspace_bytes(const cswattn_layer* layer, const cswattn_paged* paged);
 
 /* Which rows a sequence keeps when it may keep n_keep (1 .. T). For each
  * sequence b and KV head, of its L = cache_len[b] rows: the rows with

@@ -31,7 +31,7 @@ def call(lib, name, layer, paged, **change):
     a = dict(attn_paged_append=dict(rope=None, q=P, k=2 * P, v=3 * P, ve=4 * P, gate=5 * P, positions=6 * P, q_out=7 * P,
                                     k_pages=8 * P, v_pages=9 * P, weight=10 * P, position=11 * P),
              attn_paged=dict(q_out=P, k_pages=2 * P, v_pages=3 * P, O=4 * P, lse=5 * P, workspace=6 * P, size=0),
-             attn_paged_weigh=dict(q_out=P, k_pages=2 * P, lse=3 * P, weight=4 * P),
+             attn_paged_weigh=dict(q_out=P, k_pages=2 * P, lse=3 * P, weight=4 * P, workspace=5 * P, size=1 << 40),
              attn_paged_select=dict(weight=P, position=2 * P, next_pos=3 * P, n_keep=40, n_recent=4, n_moves=4 * P,
                                     src=5 * P, dst=6 * P, new_len=7 * P),
              attn_paged_move=dict(n_moves=P, src=2 * P, dst=3 * P, n_keep=40, k_pages=4 * P, v_pages=5 * P, weight=6 * P,
@@ -127,6 +127,19 @@ def test_append_refusals(lib):
     freq[5] = math.nan
     r = cs.CswattnRope(128, 0, 1.0, freq)
     assert bad(rope=ctypes.byref(r)) == cs.ERR_INVALID_ARG and b"frequency 5" in lib.cswattn_last_error()
+
+
+def test_weigh_workspace(lib):
+    for max_new, some in ((1, False), (8, False), (9, True), (100, True)):  # 4 heads a group
+        layer, paged = structs((), dict(max_new=max_new, n_tokens=300))
+        need = lib.attn_paged_weigh_workspace_bytes(ctypes.byref(layer), ctypes.byref(paged))
+        assert (need > 0) == some
+        if some:
+            assert call(lib, "attn_paged_weigh", layer, paged, size=need - 1) == cs.ERR_INVALID_ARG
+            assert b"workspace" in lib.cswattn_last_error()
+            assert call(lib, "attn_paged_weigh", layer, paged, workspace=None) == cs.ERR_INVALID_ARG
+    layer, paged = structs(dict(window=0))
+    assert lib.attn_paged_weigh_workspace_bytes(ctypes.byref(layer), ctypes.byref(paged)) == 0
 
 
 def test_attend_refusals(lib):
