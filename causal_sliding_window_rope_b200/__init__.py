@@ -381,12 +381,20 @@ def _want(device, *tensors):
     for name, t, shape, dtype in tensors:
         if t is None:
             raise ValueError(f"{name} is needed")
-        if t.dtype is not dtype or t.shape != shape:
-            raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-        if t.get_device() != device or device < 0:
-            raise ValueError(f"{name} must be a CUDA tensor on the device of the call's others, got {t.device}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
+        if t.dtype is not dtype or t.shape != shape or t.get_device() != device or device < 0 or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape {tuple(shape)} on the device of "
+                             f"the call's others, got {t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}")
+
+
+@functools.lru_cache(maxsize=256)
+def _layer_struct(*fields):
+    return ctypes.byref(LayerSpec(*fields).c())
+
+
+def _layer_ref(s: LayerSpec):
+    """The C struct of a layer, for calls that do not write to it."""
+    return _layer_struct(s.B, s.T, s.n_head, s.n_kv_head, s.head_dim, s.window, s.has_ve, s.dtype, s.rope_base, s.eps,
+                         s.softmax_scale)
 
 
 class PagedCache:
@@ -407,29 +415,34 @@ class PagedCache:
                 position = torch.zeros(*term, device=device, dtype=torch.int32) if position is None else position
         if k is not None:
             n_pages, page_size = k.shape[0], k.shape[1]
+            self.device = k.get_device()
         elif weight is not None:
             n_pages, page_size = weight.shape[0], weight.shape[2]
+            self.device = weight.get_device()
         else:
             raise ValueError("PagedCache needs n_pages and page_size, or the pools")
-        kv, term = (n_pages, page_size, spec.n_kv_head, spec.head_dim), (n_pages, spec.n_kv_head, page_size)
-        self.device = (weight if k is None else k).get_device()
-        _want(self.device, *[x for x in (("k", k, kv, torch.bfloat16), ("v", v, kv, torch.bfloat16),
-                                         ("weight", weight, term, torch.float32),
-                                         ("position", position, term, torch.int32)) if x[1] is not None])
+        self.heads = heads = (spec.n_kv_head, spec.head_dim)
+        if k is not None:
+            _want(self.device, ("k", k, (n_pages, page_size) + heads, torch.bfloat16))
+        if v is not None:
+            _want(self.device, ("v", v, (n_pages, page_size) + heads, torch.bfloat16))
+        if weight is not None:
+            _want(self.device, ("weight", weight, (n_pages, heads[0], page_size), torch.float32))
+        if position is not None:
+            _want(self.device, ("position", position, (n_pages, heads[0], page_size), torch.int32))
         self.k, self.v, self.weight, self.position = k, v, weight, position
-        self.n_pages, self.page_size, self.heads = n_pages, page_size, kv[2:]
+        self.n_pages, self.page_size = n_pages, page_size
 
-    def need(self, spec: LayerSpec, device, *names):
-        """The addresses of the pools of these names, for a call of `spec` on `device`."""
-        if self.heads != (spec.n_kv_head, spec.head_dim):
+    def need(self, spec: LayerSpec, device, *pools):
+        """Checks that these (of its) pools are there, for a call of `spec` on `device`."""
+        if self.heads[0] != spec.n_kv_head or self.heads[1] != spec.head_dim:
             raise ValueError(f"the cache holds (n_kv_head, head_dim) = {self.heads}, the layer "
                              f"{(spec.n_kv_head, spec.head_dim)}")
         if self.device != device:
             raise ValueError(f"the cache lies on cuda:{self.device}, the batch on cuda:{device}")
-        pools = [getattr(self, name) for name in names]
-        if any(t is None for t in pools):
-            raise ValueError(f"the cache has no {names[[t is None for t in pools].index(True)]}")
-        return [t.data_ptr() for t in pools]
+        for t in pools:
+            if t is None:
+                raise ValueError("the cache lacks a pool that the call needs (k, v; weight, position: track_weights)")
 
 
 class PagedBatch:
@@ -452,9 +465,10 @@ class PagedBatch:
         B, pages = self.page_table.shape
         if B != spec.B:
             raise ValueError(f"the batch has {B} sequences, the layer {spec.B}")
+        start = self.new_start
         return CswattnPaged(cache.page_size, cache.n_pages, pages, self.n_tokens, self.max_new,
                             self.page_table.data_ptr(), self.cache_len.data_ptr(),
-                            None if self.new_start is None else self.new_start.data_ptr())
+                            None if start is None else start.data_ptr())
 
 
 def _paged_call(fn, device, stream, *args):
@@ -490,15 +504,16 @@ def attn_paged_append(spec: LayerSpec, batch: PagedBatch, cache: PagedCache, q, 
         _want(dev, ("ve", ve, ks, bf), ("gate", gate, (N, Hk), bf))
     if positions is not None:
         _want(dev, ("positions", positions, (N,), torch.int32))
-    _paged_call(lib().attn_paged_append, dev, stream, ctypes.byref(spec.c()), ctypes.byref(batch.c(spec, cache)),
+    cache.need(spec, dev, cache.k, cache.v)
+    _paged_call(lib().attn_paged_append, dev, stream, _layer_ref(spec), ctypes.byref(batch.c(spec, cache)),
                 None if rope is None else ctypes.byref(rope._c), q.data_ptr(), k.data_ptr(), v.data_ptr(), _at(ve),
-                _at(gate), _at(positions), q_out.data_ptr(), *cache.need(spec, dev, "k", "v"), _at(cache.weight),
-                _at(cache.position))
+                _at(gate), _at(positions), q_out.data_ptr(), cache.k.data_ptr(), cache.v.data_ptr(),
+                _at(cache.weight), _at(cache.position))
 
 
 def attn_paged_workspace_bytes(spec: LayerSpec, batch: PagedBatch, cache: PagedCache) -> int:
     """Scratch bytes of attn_paged for this layer and the batch's sizes."""
-    return int(lib().attn_paged_workspace_bytes(ctypes.byref(spec.c()), ctypes.byref(batch.c(spec, cache))))
+    return int(lib().attn_paged_workspace_bytes(_layer_ref(spec), ctypes.byref(batch.c(spec, cache))))
 
 
 def attn_paged(spec: LayerSpec, batch: PagedBatch, cache: PagedCache, q_out, O, lse, workspace,
@@ -512,14 +527,15 @@ def attn_paged(spec: LayerSpec, batch: PagedBatch, cache: PagedCache, q_out, O, 
           ("workspace", workspace, workspace.shape, workspace.dtype))
     if workspace_bytes is None:
         workspace_bytes = workspace.numel() * workspace.element_size()
-    _paged_call(lib().attn_paged, dev, stream, ctypes.byref(spec.c()), ctypes.byref(batch.c(spec, cache)),
-                q_out.data_ptr(), *cache.need(spec, dev, "k", "v"), O.data_ptr(), lse.data_ptr(),
+    cache.need(spec, dev, cache.k, cache.v)
+    _paged_call(lib().attn_paged, dev, stream, _layer_ref(spec), ctypes.byref(batch.c(spec, cache)),
+                q_out.data_ptr(), cache.k.data_ptr(), cache.v.data_ptr(), O.data_ptr(), lse.data_ptr(),
                 workspace.data_ptr(), workspace_bytes)
 
 
 def attn_paged_weigh_workspace_bytes(spec: LayerSpec, batch: PagedBatch, cache: PagedCache) -> int:
     """Scratch bytes of attn_paged_weigh; 0 for a call of few query rows."""
-    return int(lib().attn_paged_weigh_workspace_bytes(ctypes.byref(spec.c()), ctypes.byref(batch.c(spec, cache))))
+    return int(lib().attn_paged_weigh_workspace_bytes(_layer_ref(spec), ctypes.byref(batch.c(spec, cache))))
 
 
 def attn_paged_weigh(spec: LayerSpec, batch: PagedBatch, cache: PagedCache, q_out, lse, workspace=None, stream=None):
@@ -529,8 +545,8 @@ def attn_paged_weigh(spec: LayerSpec, batch: PagedBatch, cache: PagedCache, q_ou
     import torch
     N, H, dev = batch.n_tokens, spec.n_head, batch.device
     _want(dev, ("q_out", q_out, (N, H, spec.head_dim), torch.bfloat16), ("lse", lse, (N, H), torch.float32))
-    k, weight = cache.need(spec, dev, "k", "weight")
-    layer, paged = ctypes.byref(spec.c()), ctypes.byref(batch.c(spec, cache))
+    cache.need(spec, dev, cache.k, cache.weight)
+    layer, paged = _layer_ref(spec), ctypes.byref(batch.c(spec, cache))
     if workspace is not None:
         _want(dev, ("workspace", workspace, workspace.shape, workspace.dtype))
     elif batch.max_new * H > 8 * spec.n_kv_head:  # else none is needed, whatever the sizes
@@ -542,8 +558,9 @@ def attn_paged_weigh(spec: LayerSpec, batch: PagedBatch, cache: PagedCache, q_ou
                 s = torch.cuda.ExternalStream(stream, dev) if isinstance(stream, int) else stream
                 with torch.cuda.stream(s):  # freed memory is reused in this stream's order
                     workspace = torch.empty(nbytes, dtype=torch.uint8, device=batch.page_table.device)
-    _paged_call(lib().attn_paged_weigh, dev, stream, layer, paged, q_out.data_ptr(), k, lse.data_ptr(), weight,
-                _at(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size())
+    _paged_call(lib().attn_paged_weigh, dev, stream, layer, paged, q_out.data_ptr(), cache.k.data_ptr(),
+                lse.data_ptr(), cache.weight.data_ptr(), _at(workspace),
+                0 if workspace is None else workspace.numel() * workspace.element_size())
 
 
 def attn_paged_select(spec: LayerSpec, batch: PagedBatch, cache: PagedCache, next_pos, n_keep, n_recent, n_moves,
@@ -555,8 +572,9 @@ def attn_paged_select(spec: LayerSpec, batch: PagedBatch, cache: PagedCache, nex
     i32, ms = torch.int32, (B, Hk, n_keep)
     _want(dev, ("next_pos", next_pos, (B,), i32), ("n_moves", n_moves, (B, Hk), i32), ("src", src, ms, i32),
           ("dst", dst, ms, i32), ("new_len", new_len, (B,), i32))
-    _paged_call(lib().attn_paged_select, dev, stream, ctypes.byref(spec.c()), ctypes.byref(batch.c(spec, cache)),
-                *cache.need(spec, dev, "weight", "position"), next_pos.data_ptr(), n_keep, n_recent,
+    cache.need(spec, dev, cache.weight, cache.position)
+    _paged_call(lib().attn_paged_select, dev, stream, _layer_ref(spec), ctypes.byref(batch.c(spec, cache)),
+                cache.weight.data_ptr(), cache.position.data_ptr(), next_pos.data_ptr(), n_keep, n_recent,
                 n_moves.data_ptr(), src.data_ptr(), dst.data_ptr(), new_len.data_ptr())
 
 
@@ -566,9 +584,10 @@ def attn_paged_move(spec: LayerSpec, batch: PagedBatch, cache: PagedCache, n_mov
     B, Hk, n_keep, dev = spec.B, spec.n_kv_head, src.shape[-1], batch.device
     i32, ms = torch.int32, (B, Hk, n_keep)
     _want(dev, ("n_moves", n_moves, (B, Hk), i32), ("src", src, ms, i32), ("dst", dst, ms, i32))
-    _paged_call(lib().attn_paged_move, dev, stream, ctypes.byref(spec.c()), ctypes.byref(batch.c(spec, cache)),
+    cache.need(spec, dev, cache.k, cache.v, cache.weight, cache.position)
+    _paged_call(lib().attn_paged_move, dev, stream, _layer_ref(spec), ctypes.byref(batch.c(spec, cache)),
                 n_moves.data_ptr(), src.data_ptr(), dst.data_ptr(), n_keep,
-                *cache.need(spec, dev, "k", "v", "weight", "position"))
+                cache.k.data_ptr(), cache.v.data_ptr(), cache.weight.data_ptr(), cache.position.data_ptr())
 
 
 def cswattn_sync_status(stream=None):
