@@ -202,7 +202,7 @@ cswattn_status launch_weigh_rows(const paged::WeighRowsParams& rp, const CUtenso
                                  bool prepare_only) {
   using SM = paged::WeighRowsSmem<D>;
   if (prepare_only) return set_smem(paged::weigh_rows_kernel<D, NT>, SM::kBytes + 4 * (paged::kMaxSeqs + 1));
-  launch_pdl(paged::weigh_rows_kernel<D, NT>, dim3(paged::kSMs), dim3(32 * (4 * paged::kWeighGroups + 1)),
+  launch_pdl(paged::weigh_rows_kernel<D, NT>, dim3(paged::kSMs), dim3(32 * (4 * paged::WeighGroups<NT>::value + 1)),
              static_cast<size_t>(SM::kBytes) + 4 * (rp.v.B + 1), st, mk, rp);
   return CSWATTN_OK;
 }

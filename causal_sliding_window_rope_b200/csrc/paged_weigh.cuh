@@ -45,14 +45,19 @@ struct WeighRowsSmem {
   static_assert(kBytes + 4 * (kMaxSeqs + 1) <= 232448, "shared memory per block");
 };
 
-constexpr int kWeighGroups = 2;  // groups of 4 warps that take alternate blocks: two blocks' latencies overlap
+// Groups of 4 warps that take the blocks in turn, so that the latencies of
+// several blocks (page, old weight) overlap: as many as the registers allow.
+template <int NT>
+struct WeighGroups {
+  static constexpr int value = NT <= 2 ? 4 : 2;
+};
 
 // NT: products of 8 query rows (max_rows <= 8 NT).
 template <int D, int NT>
-__global__ void __launch_bounds__(32 * (4 * kWeighGroups + 1), 1)
+__global__ void __launch_bounds__(32 * (4 * WeighGroups<NT>::value + 1), 1)
     weigh_rows_kernel(const __grid_constant__ CUtensorMap tmK, const WeighRowsParams p) {
   using SM = WeighRowsSmem<D>;
-  constexpr int NS = SM::kStages, NP = D / 64, kWarps = 4 * kWeighGroups;
+  constexpr int NS = SM::kStages, NP = D / 64, kGroups = WeighGroups<NT>::value, kWarps = 4 * kGroups;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_align1024(smem_raw);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::kOffBar);
@@ -160,7 +165,7 @@ __global__ void __launch_bounds__(32 * (4 * kWeighGroups + 1), 1)
       }
     }
     for (int t = w.t0; t < w.t1; ++t, ++at) {
-      if (at % kWeighGroups != group) continue;
+      if (at % kGroups != group) continue;
       const int stage = at % NS, use = at / NS;
       const int key0 = (first + t) * kBlk + key_w;
       // The row this lane updates (lanes 0 and 1 of each four), ahead of the products.
@@ -223,17 +228,18 @@ struct WeighTileParams {
   unsigned long long wait_ns;
 };
 
-constexpr int kWeighThreads = 320;  // producer, MMA issuer (and the query rows' terms), 8 warps of sums
+constexpr int kWeighThreads = 320;  // producer, MMA issuer, 8 warps of sums
 
 template <int D>
 struct WeighTileSmem {
   static constexpr int kPanel = 128 * 128;
   static constexpr int kOp = (D / 64) * kPanel;
+  static constexpr int kTerms = 8;                   // buffers of the query rows' terms
   static constexpr int kOffQ = kOp;                  // 2 slots
-  static constexpr int kOffTerm = 3 * kOp;           // [2][128] float
-  static constexpr int kOffHalf = kOffTerm + 1024;   // [2][128] float: the second half's sums
+  static constexpr int kOffTerm = 3 * kOp;           // [kTerms][128] float
+  static constexpr int kOffHalf = kOffTerm + kTerms * 512;   // [2][128] float: the second half's sums
   static constexpr int kOffBar = kOffHalf + 1024;
-  static constexpr int kBytes = kOffBar + 8 * 20 + 1024;
+  static constexpr int kBytes = kOffBar + 8 * (18 + kTerms) + 1024;
   static_assert(2 * (kBytes + 1024) <= 233472, "two blocks per SM");
 };
 
@@ -257,13 +263,13 @@ __global__ void __launch_bounds__(kWeighThreads, 2)
   uint64_t* q_full = k_full + 2;     // [2]
   uint64_t* q_empty = k_full + 4;    // [2]
   uint64_t* s_full = k_full + 6;     // [2] S^T buffers
-  uint64_t* s_empty = k_full + 8;    // [2] read by all sums (256 arrivals); the terms' buffer with it
-  uint64_t* t_full = k_full + 10;    // [2] terms written (32 arrivals)
-  uint64_t* h_full = k_full + 12;    // [2] the second half's sums written (128 arrivals)
-  uint64_t* h_empty = k_full + 14;   // [2] ... and read (128 arrivals)
-  uint64_t* mma_done = k_full + 16;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(k_full + 17);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(k_full + 18);
+  uint64_t* s_empty = k_full + 8;    // [2] read by all sums (256 arrivals)
+  uint64_t* h_full = k_full + 10;    // [2] the second half's sums written (128 arrivals)
+  uint64_t* h_empty = k_full + 12;   // [2] ... and read (128 arrivals)
+  uint64_t* mma_done = k_full + 14;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(k_full + 15);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(k_full + 16);
+  uint64_t* t_full = k_full + 17;    // [kTerms] -lse log2(e) of a tile's query rows written (32 arrivals)
   const View& v = p.v;
   const int warp = warp_id(), lane = lane_id(), c = blockIdx.x;
   pdl_launch_dependents();
@@ -275,10 +281,10 @@ __global__ void __launch_bounds__(kWeighThreads, 2)
       mbar_init(&q_empty[i], 1);
       mbar_init(&s_full[i], 1);
       mbar_init(&s_empty[i], 256);
-      mbar_init(&t_full[i], 32);
       mbar_init(&h_full[i], 128);
       mbar_init(&h_empty[i], 128);
     }
+    for (int i = 0; i < SM::kTerms; ++i) mbar_init(&t_full[i], 32);
     mbar_init(mma_done, 1);
     *abort_flag = 0;
     fence_barrier_init();
@@ -326,66 +332,64 @@ __global__ void __launch_bounds__(kWeighThreads, 2)
         tma_load_4d(&tmK, k_full, smem + my_panel * SM::kPanel + my_unit * p.unit * 128, 64 * my_panel, w.hk,
                     r % v.page_size, page);
       ++nk;
-      if (lane == 0) {
-        for (int t = w.t0; ok && t < w.t1; ++t, ++nq) {
-          const int slot = nq & 1;
-          if (nq > 1) ok = mbar_wait(&q_empty[slot], ((nq >> 1) - 1) & 1, wc);
-          if (!ok) break;
+      for (int t = w.t0; t < w.t1; ++t, ++nq) {
+        // The query rows' terms are loaded ahead of the wait for the slot and
+        // written behind it, which needs no barrier of their own: tile nq - 2
+        // has been multiplied, so the sums had taken tile nq - 4 before, and
+        // had left the terms of the tiles up to nq - 5.
+        static_assert(SM::kTerms >= 5, "terms' buffers");
+        const int slot = nq & 1, tb = nq % SM::kTerms, i0 = (w.first + t) * p.tpt;
+        float lse[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int qr = lane + 32 * e, i = i0 + qr / v.g;
+          lse[e] = qr < p.tpt * v.g && i < w.s.n
+                       ? p.lse[static_cast<size_t>(w.s.tok0 + i) * v.H + w.hk * v.g + qr % v.g]
+                       : 0.f;
+        }
+        if (nq > 1) ok = __all_sync(0xffffffffu, mbar_wait(&q_empty[slot], ((nq >> 1) - 1) & 1, wc));
+        if (!ok) break;
+        if (lane == 0) {
           mbar_expect_tx(&q_full[slot], p.tpt * v.g * 128 * NP);
           for (int pn = 0; pn < NP; ++pn)
             tma_load_3d(&tmQ, &q_full[slot], smem + SM::kOffQ + slot * SM::kOp + pn * SM::kPanel, 64 * pn, w.hk * v.g,
-                        w.s.tok0 + (w.first + t) * p.tpt);
+                        w.s.tok0 + i0);
         }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s_term[tb * 128 + lane + 32 * e] = lse[e] * -1.4426950408889634f;
+        mbar_arrive(&t_full[tb]);
       }
-      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
     }
     if (lane == 0) {  // every issued copy has landed
       if (nk > 0) drain_wait(k_full, (nk - 1) & 1);
       for (int i = 0; i < 2 && i < nq; ++i) drain_wait(&q_full[i], ((nq - 1 - i) >> 1) & 1);
     }
   } else if (warp == 1) {
-    // ---------------------------------------------------- S^T = K Q^T, and -lse log2(e) of the query rows
-    constexpr uint32_t idS = idesc_bf16(128, 128, 0, 0);
-    const uint64_t dK = sdesc_sw128(smem_u32(smem), 16, 1024);
-    const uint64_t dQ = sdesc_sw128(smem_u32(smem + SM::kOffQ), 16, 1024);
-    int nk = 0, nq = 0;
-    for (; ok && w.valid(); w.next()) {
-      for (int t = w.t0; t < w.t1; ++t, ++nq) {
-        const int buf = nq & 1, i0 = (w.first + t) * p.tpt;
-        float term[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = lane + 32 * e, i = i0 + r / v.g;
-          term[e] = r < p.tpt * v.g && i < w.s.n
-                        ? p.lse[static_cast<size_t>(w.s.tok0 + i) * v.H + w.hk * v.g + r % v.g] * -1.4426950408889634f
-                        : 0.f;
-        }
-        if (nq > 1) ok = __all_sync(0xffffffffu, mbar_wait(&s_empty[buf], ((nq >> 1) - 1) & 1, wc));
-        if (!ok) break;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s_term[buf * 128 + lane + 32 * e] = term[e];
-        mbar_arrive(&t_full[buf]);
-        if (lane == 0) {
-          ok = (t > w.t0 || mbar_wait(k_full, nk & 1, wc)) && mbar_wait(&q_full[buf], (nq >> 1) & 1, wc);
-          if (ok) {
-            tc_fence_after();
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint64_t off = static_cast<uint64_t>(((kk >> 2) * SM::kPanel + (kk & 3) * 32) >> 4);
-              mma_ss(tmem + buf * 128u, dK + off, dQ + static_cast<uint64_t>((buf * SM::kOp) >> 4) + off, idS,
-                     kk > 0 ? 1u : 0u);
-            }
-            mma_commit(&q_empty[buf]);
-            mma_commit(&s_full[buf]);
-            if (t + 1 == w.t1) mma_commit(k_empty);
-          }
-        }
-        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-        if (!ok) break;
-      }
-      ++nk;
-    }
+    // ---------------------------------------------------- S^T = K Q^T
     if (lane == 0) {
+      constexpr uint32_t idS = idesc_bf16(128, 128, 0, 0);
+      const uint64_t dK = sdesc_sw128(smem_u32(smem), 16, 1024);
+      const uint64_t dQ = sdesc_sw128(smem_u32(smem + SM::kOffQ), 16, 1024);
+      int nk = 0, nq = 0;
+      for (; ok && w.valid(); w.next(), ++nk) {
+        ok = mbar_wait(k_full, nk & 1, wc);
+        for (int t = w.t0; ok && t < w.t1; ++t, ++nq) {
+          const int buf = nq & 1;
+          ok = mbar_wait(&q_full[buf], (nq >> 1) & 1, wc) &&
+               (nq < 2 || mbar_wait(&s_empty[buf], ((nq >> 1) - 1) & 1, wc));
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t off = static_cast<uint64_t>(((kk >> 2) * SM::kPanel + (kk & 3) * 32) >> 4);
+            mma_ss(tmem + buf * 128u, dK + off, dQ + static_cast<uint64_t>((buf * SM::kOp) >> 4) + off, idS,
+                   kk > 0 ? 1u : 0u);
+          }
+          mma_commit(&q_empty[buf]);
+          mma_commit(&s_full[buf]);
+        }
+        if (ok) mma_commit(k_empty);
+      }
       mma_commit(mma_done);
       drain_wait(mma_done, 0);
     }
@@ -423,7 +427,7 @@ __global__ void __launch_bounds__(kWeighThreads, 2)
         const int past = key - w.s.L - i0;
         const int a = max(0, past * v.g) - 64 * half;
         const int b = min(min(p.tpt, w.s.n - i0) * v.g, (past + v.W) * v.g) - 1 - 64 * half;
-        ok = __all_sync(0xffffffffu, mbar_wait(&t_full[buf], (nq >> 1) & 1, wc) &&
+        ok = __all_sync(0xffffffffu, mbar_wait(&t_full[nq % SM::kTerms], (nq / SM::kTerms) & 1, wc) &&
                                          mbar_wait(&s_full[buf], (nq >> 1) & 1, wc));
         if (!ok) break;
         tc_fence_after();
@@ -432,13 +436,15 @@ __global__ void __launch_bounds__(kWeighThreads, 2)
         tmem_ld32(tS + buf * 128, sv[0]);
         tmem_ld32(tS + buf * 128 + 32, sv[1]);
         tmem_ld_wait();
+        tc_fence_before();
+        mbar_arrive(&s_empty[buf]);  // the scores are in registers: the next product may overwrite them
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if (!__any_sync(0xffffffffu, a <= 32 * h + 31 && b >= 32 * h)) continue;  // nobody sees these
           const bool all = __all_sync(0xffffffffu, a <= 32 * h && b >= 32 * h + 31);
 #pragma unroll
           for (int e4 = 0; e4 < 8; ++e4) {
-            const float4 l4 = *reinterpret_cast<const float4*>(&s_term[buf * 128 + 64 * half + h * 32 + e4 * 4]);
+            const float4 l4 = *reinterpret_cast<const float4*>(&s_term[nq % SM::kTerms * 128 + 64 * half + h * 32 + e4 * 4]);
             const float x0 = ex2(fmaf(__uint_as_float(sv[h][4 * e4]), c2, l4.x));
             const float x1 = ex2(fmaf(__uint_as_float(sv[h][4 * e4 + 1]), c2, l4.y));
             const float x2 = ex2(fmaf(__uint_as_float(sv[h][4 * e4 + 2]), c2, l4.z));
@@ -458,8 +464,6 @@ __global__ void __launch_bounds__(kWeighThreads, 2)
           }
         }
         total += (part[0] + part[1]) + (part[2] + part[3]);
-        tc_fence_before();
-        mbar_arrive(&s_empty[buf]);
       }
       if (!ok) break;
       // The second half hands its sum over; the first adds and writes.
