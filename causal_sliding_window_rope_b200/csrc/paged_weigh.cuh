@@ -315,6 +315,15 @@ __global__ void __launch_bounds__(kWeighThreads, 2)
     }
     const int boxes = (128 / p.unit) * NP;
     const int my_unit = lane / NP, my_panel = lane % NP;
+    int q_tok[4], q_head[4];  // token of the tile and head of the group of this lane's query rows
+    bool q_in[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int qr = lane + 32 * e;
+      q_tok[e] = qr / v.g;
+      q_head[e] = qr % v.g;
+      q_in[e] = qr < p.tpt * v.g;
+    }
     int nk = 0, nq = 0;
     for (; ok && w.valid(); w.next()) {
       const int lo = max(0, w.s.L - v.W + 1), end = w.s.L + w.s.n;
@@ -332,32 +341,35 @@ __global__ void __launch_bounds__(kWeighThreads, 2)
         tma_load_4d(&tmK, k_full, smem + my_panel * SM::kPanel + my_unit * p.unit * 128, 64 * my_panel, w.hk,
                     r % v.page_size, page);
       ++nk;
-      for (int t = w.t0; t < w.t1; ++t, ++nq) {
-        // The query rows' terms are loaded ahead of the wait for the slot and
-        // written behind it, which needs no barrier of their own: tile nq - 2
-        // has been multiplied, so the sums had taken tile nq - 4 before, and
-        // had left the terms of the tiles up to nq - 5.
-        static_assert(SM::kTerms >= 5, "terms' buffers");
-        const int slot = nq & 1, tb = nq % SM::kTerms, i0 = (w.first + t) * p.tpt;
-        float lse[4];
+      // Terms of the query rows lane, lane + 32, ... of a tile: loaded one tile
+      // ahead, written behind the wait for the tile's slot, which needs no
+      // barrier of their own: tile nq - 2 has been multiplied, so the sums had
+      // taken tile nq - 4 before, and had left the terms up to tile nq - 5.
+      static_assert(SM::kTerms >= 5, "terms' buffers");
+      float term[4];
+      auto load_terms = [&](int t) {
+        const int i0 = (w.first + t) * p.tpt;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int qr = lane + 32 * e, i = i0 + qr / v.g;
-          lse[e] = qr < p.tpt * v.g && i < w.s.n
-                       ? p.lse[static_cast<size_t>(w.s.tok0 + i) * v.H + w.hk * v.g + qr % v.g]
-                       : 0.f;
+          const bool in = q_in[e] && i0 + q_tok[e] < w.s.n;
+          term[e] = in ? p.lse[static_cast<size_t>(w.s.tok0 + i0 + q_tok[e]) * v.H + w.hk * v.g + q_head[e]] : 0.f;
         }
+      };
+      load_terms(w.t0);
+      for (int t = w.t0; t < w.t1; ++t, ++nq) {
+        const int slot = nq & 1, tb = nq % SM::kTerms;
         if (nq > 1) ok = __all_sync(0xffffffffu, mbar_wait(&q_empty[slot], ((nq >> 1) - 1) & 1, wc));
         if (!ok) break;
         if (lane == 0) {
           mbar_expect_tx(&q_full[slot], p.tpt * v.g * 128 * NP);
           for (int pn = 0; pn < NP; ++pn)
             tma_load_3d(&tmQ, &q_full[slot], smem + SM::kOffQ + slot * SM::kOp + pn * SM::kPanel, 64 * pn, w.hk * v.g,
-                        w.s.tok0 + i0);
+                        w.s.tok0 + (w.first + t) * p.tpt);
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s_term[tb * 128 + lane + 32 * e] = lse[e] * -1.4426950408889634f;
+        for (int e = 0; e < 4; ++e) s_term[tb * 128 + lane + 32 * e] = term[e] * -1.4426950408889634f;
         mbar_arrive(&t_full[tb]);
+        if (t + 1 < w.t1) load_terms(t + 1);
       }
     }
     if (lane == 0) {  // every issued copy has landed
