@@ -195,88 +195,87 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (q_issued > 0) drain_wait(q_full, (q_issued - 1) & 1);
       }
     } else if (warp == 1) {
-      if (lane == 0) {
-        // ---------------------------------------------- MMA issuer
-        constexpr uint32_t idS = idesc_bf16(128, 128, 0, 0);  // Q K^T: both K-major
-        constexpr uint32_t idPV = idesc_bf16(128, D, 0, 1);   // P V: V MN-major
-        const uint64_t dQ0 = sdesc_sw128(smem_u32(smem), 16, 1024);
-        const uint64_t dK0 = sdesc_sw128(smem_u32(smem + SM::kOffKV), 16, 1024);
-        const uint64_t dV0 = sdesc_sw128(smem_u32(smem + SM::kOffKV), SM::kPanel, 1024);
-        int base = 0, segs = 0;  // blocks of earlier segments; segments
-        int np[2] = {0, 0};      // P tiles taken, per tile
-        bool ok = true;
-        for (TileWalk w(p, run); ok && w.valid(); w.next(), ++segs) {
-          const int lo = w.first + w.t0, hi = w.first + w.t1 - 1;
-          int lo_t[2], hi_t[2];
-          bool on[2];
-          for (int X = 0; X < 2; ++X) on[X] = w.tile(X, lo_t[X], hi_t[X]);
-          auto ring = [&](int j, int kind, int& slot, int& use) {
-            const int i = 2 * (base + j - lo) + kind;
-            slot = i % NS;
-            use = i / NS;
-          };
-          auto issue_S = [&](int X, int j) -> bool {
-            int s, use;
-            ring(j, 0, s, use);
-            if (!mbar_wait(&kv_full[s], use & 1, wc)) return false;
-            tc_fence_after();
-            const uint64_t qd = dQ0 + static_cast<uint64_t>((X * SM::kOp) >> 4);
-            const uint64_t kd = dK0 + static_cast<uint64_t>((s * SM::kOp) >> 4);
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint64_t off = static_cast<uint64_t>(((kk >> 2) * SM::kPanel + (kk & 3) * 32) >> 4);
-              mma_ss(tmem + static_cast<uint32_t>(X) * 128u, qd + off, kd + off, idS, kk > 0 ? 1u : 0u);
-            }
-            mma_commit(&s_full[X]);
-            return true;
-          };
-          auto issue_PV = [&](int X, int j) -> bool {
-            int s, use;
-            ring(j, 1, s, use);
-            if (!mbar_wait(&kv_full[s], use & 1, wc)) return false;
-            if (!mbar_wait(&p_full[X], np[X] & 1, wc)) return false;
-            ++np[X];
-            tc_fence_after();
-            const uint64_t vd = dV0 + static_cast<uint64_t>((s * SM::kOp) >> 4);
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              mma_ts(tmem + 256u + static_cast<uint32_t>(X) * 128u, tmem + static_cast<uint32_t>(X) * 128u + kk * 8,
-                     vd + static_cast<uint64_t>((kk * 2048) >> 4), idPV, (j > lo_t[X] || kk > 0) ? 1u : 0u);
-            return true;
-          };
-          int rs, ru;
-          ok = mbar_wait(q_full, segs & 1, wc);
-          if (ok) tc_fence_after();
-          for (int X = 0; X < 2 && ok; ++X)
-            if (on[X] && lo_t[X] == lo) ok = issue_S(X, lo);
-          if (!ok) break;
-          ring(lo, 0, rs, ru);
-          mma_commit(&kv_empty[rs]);
-          if (lo == hi) mma_commit(q_empty);
-          for (int j = lo; ok && j <= hi; ++j) {
-            for (int X = 0; X < 2 && ok; ++X) {
-              if (!on[X]) continue;
-              if (j >= lo_t[X] && j <= hi_t[X]) {
-                ok = issue_PV(X, j);
-                if (ok && j == hi_t[X]) mma_commit(&o_full[X]);
-              }
-              if (ok && j + 1 >= lo_t[X] && j + 1 <= hi_t[X]) ok = issue_S(X, j + 1);
-            }
-            if (!ok) break;
-            ring(j, 1, rs, ru);
-            mma_commit(&kv_empty[rs]);  // V_j consumed
-            if (j + 1 <= hi) {
-              ring(j + 1, 0, rs, ru);
-              mma_commit(&kv_empty[rs]);  // K_j+1 consumed
-              if (j + 1 == hi) mma_commit(q_empty);
-            }
-          }
-          base += hi - lo + 1;
+      // ------------------------------------------------ MMA issuer (the whole warp, one lane of which issues)
+      constexpr uint32_t idS = idesc_bf16(128, 128, 0, 0);  // Q K^T: both K-major
+      constexpr uint32_t idPV = idesc_bf16(128, D, 0, 1);   // P V: V MN-major
+      const uint32_t leader = elect_one();
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint64_t dQ0 = sdesc_sw128(smem_u32(smem), 16, 1024);
+      const uint64_t dK0 = sdesc_sw128(smem_u32(smem + SM::kOffKV), 16, 1024);
+      const uint64_t dV0 = sdesc_sw128(smem_u32(smem + SM::kOffKV), SM::kPanel, 1024);
+      int ks = 0, ku = 0;  // ring position of the block's K; its V is the next one
+      int segs = 0, np[2] = {0, 0};  // segments; P tiles taken, per tile
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, int parity) {
+        return __all_sync(0xffffffffu, mbar_wait(bar, static_cast<uint32_t>(parity), wc));
+      };
+      auto after = [&](int& slot, int& use) {
+        if (++slot == NS) {
+          slot = 0;
+          ++use;
         }
-        // All issued MMAs complete before TMEM is released.
-        mma_commit(mma_done);
-        drain_wait(mma_done, 0);
+      };
+      auto issue_S = [&](int X, int slot) {
+        const uint64_t qd = dQ0 + static_cast<uint64_t>((X * SM::kOp) >> 4);
+        const uint64_t kd = dK0 + static_cast<uint64_t>(__shfl_sync(0xffffffffu, slot, 0) * (SM::kOp >> 4));
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint64_t off = static_cast<uint64_t>(((kk >> 2) * SM::kPanel + (kk & 3) * 32) >> 4);
+          mma_ss_warp(tm + static_cast<uint32_t>(X) * 128u, qd + off, kd + off, idS, kk > 0 ? 1u : 0u, leader);
+        }
+        mma_commit_warp(&s_full[X], leader);
+      };
+      auto issue_PV = [&](int X, int slot, uint32_t add) {
+        const uint64_t vd = dV0 + static_cast<uint64_t>(__shfl_sync(0xffffffffu, slot, 0) * (SM::kOp >> 4));
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma_ts_warp(tm + 256u + static_cast<uint32_t>(X) * 128u, tm + static_cast<uint32_t>(X) * 128u + kk * 8,
+                      vd + static_cast<uint64_t>((kk * 2048) >> 4), idPV, kk > 0 ? 1u : add, leader);
+      };
+      for (TileWalk w(p, run); ok && w.valid(); w.next(), ++segs) {
+        const int lo = w.first + w.t0, hi = w.first + w.t1 - 1;
+        int lo_t[2], hi_t[2];
+        bool on[2];
+#pragma unroll
+        for (int X = 0; X < 2; ++X) on[X] = w.tile(X, lo_t[X], hi_t[X]);
+        ok = wait(q_full, segs & 1) && wait(&kv_full[ks], ku & 1);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int X = 0; X < 2; ++X)
+          if (on[X] && lo_t[X] == lo) issue_S(X, ks);
+        mma_commit_warp(&kv_empty[ks], leader);
+        if (lo == hi) mma_commit_warp(q_empty, leader);
+        for (int j = lo; j <= hi; ++j) {
+          int vs = ks, vu = ku;  // V_j, then K_j+1
+          after(vs, vu);
+          ks = vs;
+          ku = vu;
+          after(ks, ku);
+          ok = wait(&kv_full[vs], vu & 1) && (j == hi || wait(&kv_full[ks], ku & 1));
+          if (!ok) break;
+#pragma unroll
+          for (int X = 0; X < 2; ++X) {
+            if (on[X] && j >= lo_t[X] && j <= hi_t[X]) {
+              ok = ok && wait(&p_full[X], np[X] & 1);
+              if (!ok) break;
+              ++np[X];
+              tc_fence_after();
+              issue_PV(X, vs, j > lo_t[X] ? 1u : 0u);
+              if (j == hi_t[X]) mma_commit_warp(&o_full[X], leader);
+            }
+            if (on[X] && j + 1 >= lo_t[X] && j + 1 <= hi_t[X]) issue_S(X, ks);
+          }
+          if (!ok) break;
+          mma_commit_warp(&kv_empty[vs], leader);  // V_j consumed
+          if (j < hi) mma_commit_warp(&kv_empty[ks], leader);  // K_j+1 consumed
+          if (j + 1 == hi) mma_commit_warp(q_empty, leader);
+        }
       }
+      // All issued MMAs complete before TMEM is released.
+      mma_commit_warp(mma_done, leader);
+      if (leader) drain_wait(mma_done, 0);
+      __syncwarp();
     }
   } else {
     regs_inc<kTileRegHi>();
