@@ -24,6 +24,7 @@ constexpr int kUnit = 16;        // rows: a page holds whole units, so a unit ne
 struct View {
   int B, T, H, Hk, g, W;
   int page_size, n_pages, pages_per_seq;
+  int page_shift;  // log2(page_size), or -1
   int n_tokens, max_new;
   const int *page_table, *cache_len, *new_start;
 };
@@ -55,6 +56,15 @@ __device__ __forceinline__ int page_at(const View& v, int b, int entry) {
   if (p >= 0 && p < v.n_pages) return p;
   atomicOr(&g_status, kStatusRange);
   return -1;
+}
+
+// A row's entry of the page table and its slot in the page: shifts where the
+// page is a power of two (a division costs some 20 instructions).
+__device__ __forceinline__ int page_entry(const View& v, int row) {
+  return v.page_shift >= 0 ? row >> v.page_shift : row / v.page_size;
+}
+__device__ __forceinline__ int page_slot(const View& v, int row) {
+  return v.page_shift >= 0 ? row & (v.page_size - 1) : row % v.page_size;
 }
 
 // Row of a (pages, page_size, Hk) pool of K or V rows (in units of head_dim

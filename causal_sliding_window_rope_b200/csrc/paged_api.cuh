@@ -51,6 +51,9 @@ cswattn_status check_paged(const cswattn_layer* layer, const cswattn_paged* pg, 
   v->g = s->g;
   v->W = s->W;
   v->page_size = pg->page_size;
+  v->page_shift = -1;
+  for (int i = 4; i < 31; ++i)
+    if (pg->page_size == 1 << i) v->page_shift = i;
   v->n_pages = pg->n_pages;
   v->pages_per_seq = pg->pages_per_seq;
   v->n_tokens = pg->n_tokens;
@@ -523,8 +526,7 @@ cswattn_status attn_paged_move(const cswattn_layer* layer, const cswattn_paged* 
   const int most = std::min(n_keep, s.T - n_keep);
   if (most == 0) return CSWATTN_OK;
   const int per = paged::kMoveThreads / (s.D / 8) * paged::kMoveBatch;
-  const int share = std::max(1, paged::kMoveCtas / (s.B * s.Hk));
-  const dim3 grid(std::min(share, (most + per - 1) / per), s.Hk, s.B);
+  const dim3 grid(std::min(paged::kMoveMaxCtas, (most + per - 1) / per), s.Hk, s.B);
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   {
     ScopedTiming tm(CSWATTN_K_DECODE, cs);

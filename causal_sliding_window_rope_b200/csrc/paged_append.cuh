@@ -70,8 +70,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
       Seq s;
       if (seq_load(v, b, false, s)) {
         const int row = s.L + (t0 + tt - s.tok0);
-        page = page_at(v, b, row / v.page_size);
-        s_slot[tt] = row % v.page_size;
+        page = page_at(v, b, page_entry(v, row));
+        s_slot[tt] = page_slot(v, row);
         s_pos[tt] = p.positions ? p.positions[t0 + tt] : row;
       }
     }

@@ -42,11 +42,12 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Shared memory of the cluster's CTA `rank` at the place of p.
-__device__ __forceinline__ uint32_t peer_load(const void* p, int rank) {
-  uint32_t a, y;
+// Two words of shared memory of the cluster's CTA `rank` at the place of p.
+__device__ __forceinline__ uint2 peer_load2(const void* p, int rank) {
+  uint32_t a;
+  uint2 y;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(y) : "r"(a) : "memory");
+  asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(y.x), "=r"(y.y) : "r"(a) : "memory");
   return y;
 }
 
@@ -58,10 +59,11 @@ __device__ __forceinline__ uint32_t peer_load(const void* p, int rank) {
 // over up to 8 SMs. Every path of a cluster's CTAs meets the same barriers.
 __global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectParams p) {
   extern __shared__ uint32_t s_key[];
-  __shared__ uint32_t s_hist[2][kBins];  // two, so that a pass needs one meeting of the cluster
+  __shared__ __align__(16) uint32_t s_hist[2][kBins];  // two, so that a pass needs one meeting of the cluster
   __shared__ uint32_t s_warp[32];
   __shared__ uint32_t s_pick[2];
-  __shared__ uint32_t s_count[3];        // this CTA's ties, holes, movers
+  __shared__ __align__(8) uint2 s_count[2];  // this CTA's ties; its holes and movers
+  __shared__ uint2 s_before, s_all;          // ... of the CTAs before it, and of all
   const View& v = p.v;
   const int rank = blockIdx.x, ranks = gridDim.x, hk = blockIdx.y, b = blockIdx.z;
   const int warp = warp_id(), lane = lane_id(), tid = threadIdx.x;
@@ -90,9 +92,9 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectPara
   const long long recent = static_cast<long long>(p.next_pos[b]) - p.n_recent;
   auto compute = [&](int i) -> uint32_t {
     const int r = base + i;
-    const int page = page_at(v, b, r / v.page_size);
+    const int page = page_at(v, b, page_entry(v, r));
     if (page < 0) return 0u;
-    const size_t at = term_index(v, page, r % v.page_size, hk);
+    const size_t at = term_index(v, page, page_slot(v, r), hk);
     const float w = p.weight[at];
     return p.position[at] >= recent ? 0xFFFFFFFFu : weight_order(w);
   };
@@ -125,15 +127,14 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectPara
     }
     cluster_sync();
     // Thread t holds bins 2t and 2t + 1 of all CTAs; suffix sums from the top.
-    uint32_t h0 = 0u, h1 = 0u;
-    if (ranks == 1) {
-      h0 = hist[2 * tid];
-      h1 = hist[2 * tid + 1];
-    } else {
-      for (int k = 0; k < ranks; ++k) {
-        h0 += peer_load(&hist[2 * tid], k);
-        h1 += peer_load(&hist[2 * tid + 1], k);
-      }
+    // (each CTA starts with its own counts, so that not all read the same one)
+    uint32_t h0 = hist[2 * tid], h1 = hist[2 * tid + 1];
+#pragma unroll
+    for (int j = 1; j < kSelectMaxCluster; ++j) {
+      if (j >= ranks) break;
+      const uint2 h = peer_load2(&hist[2 * tid], (rank + j) % ranks);
+      h0 += h.x;
+      h1 += h.y;
     }
     uint32_t inc = h0 + h1;
 #pragma unroll
@@ -183,24 +184,33 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectPara
     total = __shfl_sync(0xffffffffu, inc, 31);
     return __shfl_sync(0xffffffffu, inc - x, warp);
   };
-  auto before_cta = [&](int which, uint32_t& total) -> uint32_t {  // after the counts have met
-    uint32_t sum = 0u;
-    total = 0u;
-    for (int k = 0; k < ranks; ++k) {
-      const uint32_t x = ranks == 1 ? s_count[which] : peer_load(&s_count[which], k);
-      if (k < rank) sum += x;
-      total += x;
+  auto exchange = [&](int which) {  // the cluster's counts: lane k of warp 0 reads CTA k's
+    cluster_sync();
+    if (warp == 0) {
+      uint2 x = lane < ranks ? peer_load2(&s_count[which], lane) : make_uint2(0u, 0u);
+      uint2 b = lane < rank ? x : make_uint2(0u, 0u);
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) {
+        x.x += __shfl_xor_sync(0xffffffffu, x.x, o);
+        x.y += __shfl_xor_sync(0xffffffffu, x.y, o);
+        b.x += __shfl_xor_sync(0xffffffffu, b.x, o);
+        b.y += __shfl_xor_sync(0xffffffffu, b.y, o);
+      }
+      if (lane == 0) {
+        s_before = b;
+        s_all = x;
+      }
     }
-    return sum;
+    __syncthreads();
   };
   const uint32_t below = (1u << lane) - 1u;
-  uint32_t eq = 0u, cta_total, all;
+  uint32_t eq = 0u, cta_total;
   for (int i0 = i_lo; i0 < i_hi; i0 += 32)
     eq += __popc(__ballot_sync(0xffffffffu, i0 + lane < i_hi && key(i0 + lane) == prefix));
   uint32_t eq_before = before_warp(eq, cta_total);
-  if (tid == 0) s_count[0] = cta_total;
-  cluster_sync();
-  eq_before += before_cta(0, all);
+  if (tid == 0) s_count[0] = make_uint2(cta_total, 0u);
+  exchange(0);
+  eq_before += s_before.x;
   uint32_t hole_at = 0u, mover_at = 0u, total = 0u;
   for (int pass = 0; pass < 2; ++pass) {
     uint32_t e = eq_before, nh = hole_at, nm = mover_at;
@@ -222,13 +232,14 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectPara
       nm += __popc(mm);
     }
     if (pass == 0) {
+      uint32_t cta_movers;
       hole_at = before_warp(nh, cta_total);
-      if (tid == 0) s_count[1] = cta_total;
-      mover_at = before_warp(nm, cta_total);
-      if (tid == 0) s_count[2] = cta_total;
-      cluster_sync();
-      hole_at += before_cta(1, all);
-      mover_at += before_cta(2, total);
+      mover_at = before_warp(nm, cta_movers);
+      if (tid == 0) s_count[1] = make_uint2(cta_total, cta_movers);
+      exchange(1);
+      hole_at += s_before.x;
+      mover_at += s_before.y;
+      total = s_all.y;
     }
   }
   if (lead && tid == 0) p.n_moves[head] = static_cast<int>(total);
@@ -247,7 +258,7 @@ struct MoveParams {
 };
 
 constexpr int kMoveThreads = 256;
-constexpr int kMoveCtas = 8 * kSMs;  // of a call, about: a head's moves are spread over its share of them
+constexpr int kMoveMaxCtas = 256;    // of a head: its moves are spread over them
 constexpr int kMoveBatch = 4;        // moves a group of lanes has in flight
 
 // D / 8 lanes copy one row of K and of V, 16 bytes each, kMoveBatch rows at a
@@ -283,8 +294,8 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const MoveParams p) 
         atomicOr(&g_status, kStatusRange);
         continue;
       }
-      pf[j] = page_at(v, b, from[j] / v.page_size);
-      pt[j] = page_at(v, b, to[j] / v.page_size);
+      pf[j] = page_at(v, b, page_entry(v, from[j]));
+      pt[j] = page_at(v, b, page_entry(v, to[j]));
     }
     uint4 kk[kMoveBatch], vv[kMoveBatch];
     float w[kMoveBatch];
@@ -292,7 +303,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const MoveParams p) 
 #pragma unroll
     for (int j = 0; j < kMoveBatch; ++j) {
       if (pf[j] < 0 || pt[j] < 0) continue;
-      const int slot = from[j] % v.page_size;
+      const int slot = page_slot(v, from[j]);
       const size_t a = kv_index(v, pf[j], slot, hk) * D + sub * 8;
       kk[j] = *reinterpret_cast<const uint4*>(p.k_pages + a);
       vv[j] = *reinterpret_cast<const uint4*>(p.v_pages + a);
@@ -304,7 +315,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const MoveParams p) 
 #pragma unroll
     for (int j = 0; j < kMoveBatch; ++j) {
       if (pf[j] < 0 || pt[j] < 0) continue;
-      const int slot = to[j] % v.page_size;
+      const int slot = page_slot(v, to[j]);
       const size_t z = kv_index(v, pt[j], slot, hk) * D + sub * 8;
       *reinterpret_cast<uint4*>(p.k_pages + z) = kk[j];
       *reinterpret_cast<uint4*>(p.v_pages + z) = vv[j];

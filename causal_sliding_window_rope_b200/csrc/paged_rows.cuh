@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(32 * (kKeyGroups * MB + 1), 1)
       auto lookup = [&](int t) -> int {  // page of this lane's unit, or past the pool
         const int r = (first + t) * kBlk + my_unit * p.unit;
         if (lane >= boxes || r >= end || r + p.unit <= lo) return v.n_pages;
-        const int page = page_at(v, w.b, r / v.page_size);
+        const int page = page_at(v, w.b, page_entry(v, r));
         return page < 0 ? v.n_pages : page;
       };
       int page = lookup(w.t0);
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(32 * (kKeyGroups * MB + 1), 1)
         }
         __syncwarp();
         if (lane < boxes) {
-          const int slot = ((first + t) * kBlk + my_unit * p.unit) % v.page_size;
+          const int slot = page_slot(v, (first + t) * kBlk + my_unit * p.unit);
           uint8_t* dst = my_dst + stage * SM::kStage;
           tma_load_4d(&tmK, &full_k[stage], dst, 64 * my_panel, w.hk, slot, page);
           tma_load_4d(&tmV, &full_v[stage], dst + SM::kOp, 64 * my_panel, w.hk, slot, page);

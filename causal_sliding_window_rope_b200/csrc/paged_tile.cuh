@@ -147,13 +147,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         auto lookup = [&](int t) -> int {  // page of this lane's unit, or past the pool
           const int r = (w.first + t) * 128 + my_unit * p.unit;
           if (lane >= boxes || r >= end || r + p.unit <= lo) return v.n_pages;
-          const int page = page_at(v, b, r / v.page_size);
+          const int page = page_at(v, b, page_entry(v, r));
           return page < 0 ? v.n_pages : page;
         };
         int page = lookup(w.t0);
         for (int t = w.t0; ok && t < w.t1; ++t) {
           const int next = t + 1 < w.t1 ? lookup(t + 1) : 0;
-          const int row_slot = ((w.first + t) * 128 + my_unit * p.unit) % v.page_size;
+          const int row_slot = page_slot(v, (w.first + t) * 128 + my_unit * p.unit);
 #pragma unroll
           for (int kind = 0; kind < 2; ++kind) {
             if (use > 0) ok = ok && __all_sync(0xffffffffu, mbar_wait(&kv_empty[slot], (use - 1) & 1, wc));

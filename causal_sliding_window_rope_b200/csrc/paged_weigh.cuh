@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(32 * (4 * WeighGroups<NT>::value + 1), 1)
       auto lookup = [&](int t) -> int {
         const int r = (first + t) * kBlk + my_unit * p.unit;
         if (lane >= boxes || r >= end || r + p.unit <= lo) return v.n_pages;
-        const int page = page_at(v, w.b, r / v.page_size);
+        const int page = page_at(v, w.b, page_entry(v, r));
         return page < 0 ? v.n_pages : page;
       };
       int page = lookup(w.t0);
@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(32 * (4 * WeighGroups<NT>::value + 1), 1)
         __syncwarp();
         if (lane < boxes)
           tma_load_4d(&tmK, &full[stage], my_dst + stage * SM::kStage, 64 * my_panel, w.hk,
-                      ((first + t) * kBlk + my_unit * p.unit) % v.page_size, page);
+                      page_slot(v, (first + t) * kBlk + my_unit * p.unit), page);
         ++issued;
         page = next;
         if (++stage == NS) {
@@ -174,9 +174,9 @@ __global__ void __launch_bounds__(32 * (4 * WeighGroups<NT>::value + 1), 1)
       float* dst = nullptr;
       float old = 0.f;
       if (mine) {
-        const int page = page_at(v, w.b, key / v.page_size);
+        const int page = page_at(v, w.b, page_entry(v, key));
         if (page >= 0) {
-          dst = p.weight + term_index(v, page, key % v.page_size, w.hk);
+          dst = p.weight + term_index(v, page, page_slot(v, key), w.hk);
           old = *dst;
         }
       }
@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kWeighThreads, 2)
       const int r = w.units.first_row(v, w.s, w.u) + my_unit * p.unit;
       int page = v.n_pages;  // past the pool: zeros
       if (lane < boxes && r < end && r + p.unit > lo) {
-        page = page_at(v, w.seq(), r / v.page_size);
+        page = page_at(v, w.seq(), page_entry(v, r));
         if (page < 0) page = v.n_pages;
       }
       if (nk > 0) ok = __all_sync(0xffffffffu, mbar_wait(k_empty, (nk - 1) & 1, wc));
@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(kWeighThreads, 2)
       __syncwarp();
       if (lane < boxes)
         tma_load_4d(&tmK, k_full, smem + my_panel * SM::kPanel + my_unit * p.unit * 128, 64 * my_panel, w.hk,
-                    r % v.page_size, page);
+                    page_slot(v, r), page);
       ++nk;
       // Terms of the query rows lane, lane + 32, ... of a tile: loaded one tile
       // ahead, written behind the wait for the tile's slot, which needs no
@@ -423,9 +423,9 @@ __global__ void __launch_bounds__(kWeighThreads, 2)
         if (!whole) {
           place = p.part + static_cast<size_t>(2 * c + (nu == 0 ? 0 : 1)) * 128 + r;
         } else if (key < end && key > w.s.L - v.W) {
-          const int page = page_at(v, w.seq(), key / v.page_size);
+          const int page = page_at(v, w.seq(), page_entry(v, key));
           if (page >= 0) {
-            place = p.weight + term_index(v, page, key % v.page_size, w.hk);
+            place = p.weight + term_index(v, page, page_slot(v, key), w.hk);
             old = *place;
           }
         }
@@ -515,11 +515,11 @@ __global__ void __launch_bounds__(128) weigh_join_kernel(const __grid_constant__
   seq_load(v, b, false, s);
   const int key = RowUnits{p.tpt}.first_row(v, s, cut.st.unit) + threadIdx.x;
   if (key >= s.L + s.n || key <= s.L - v.W) return;
-  const int page = page_at(v, b, key / v.page_size);
+  const int page = page_at(v, b, page_entry(v, key));
   if (page < 0) return;
   float total = 0.f;
   for (int k = cut.c - 1; k <= cut.last; ++k) total += p.part[static_cast<size_t>(cut.slot(k)) * 128 + threadIdx.x];
-  p.weight[term_index(v, page, key % v.page_size, cut.st.hk)] += total;
+  p.weight[term_index(v, page, page_slot(v, key), cut.st.hk)] += total;
 }
 
 }  // namespace paged
