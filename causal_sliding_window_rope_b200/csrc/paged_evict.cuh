@@ -42,7 +42,13 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Two words of shared memory of the cluster's CTA `rank` at the place of p.
+// One or two words of shared memory of the cluster's CTA `rank` at the place of p.
+__device__ __forceinline__ uint32_t peer_load(const void* p, int rank) {
+  uint32_t a, y;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(y) : "r"(a) : "memory");
+  return y;
+}
 __device__ __forceinline__ uint2 peer_load2(const void* p, int rank) {
   uint32_t a;
   uint2 y;
@@ -53,17 +59,20 @@ __device__ __forceinline__ uint2 peer_load2(const void* p, int rank) {
 
 // A cluster of gridDim.x CTAs = (sequence, KV head), each with a run of
 // consecutive rows. The n_keep-th largest key comes from three radix passes
-// (11, 11, 10 bits): each CTA counts its rows' digits, the counts of all
-// CTAs are read through the cluster's shared memory. Bound by latency, so the
-// rows are read once (keys stay in shared memory) and long heads are spread
-// over up to 8 SMs. Every path of a cluster's CTAs meets the same barriers.
+// (11, 11, 10 bits): each CTA counts its rows' digits, the sums of 32 bins
+// are read from all CTAs' shared memory, then the 32 bins of the one that
+// holds the key. Bound by latency, so the rows are read once (keys stay in
+// shared memory), long heads are spread over up to 8 SMs, and what the
+// others have to know of a CTA's rows is exchanged once. Every path of a
+// cluster's CTAs meets the same barriers.
 __global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectParams p) {
   extern __shared__ uint32_t s_key[];
-  __shared__ __align__(16) uint32_t s_hist[2][kBins];  // two, so that a pass needs one meeting of the cluster
-  __shared__ uint32_t s_warp[32];
+  __shared__ uint32_t s_hist[2][kBins];          // two, so that a pass needs one meeting of the cluster
+  __shared__ __align__(8) uint32_t s_sum[2][64];  // of 32 bins each
   __shared__ uint32_t s_pick[2];
-  __shared__ __align__(8) uint2 s_count[2];  // this CTA's ties; its holes and movers
-  __shared__ uint2 s_before, s_all;          // ... of the CTAs before it, and of all
+  __shared__ uint32_t s_warp[4][32];             // of each warp's rows: ties and larger keys, below n_keep and past it
+  __shared__ __align__(8) uint2 s_count[2];      // the same of this CTA
+  __shared__ uint32_t s_before[3], s_total;      // ties, holes, movers of the CTAs before it; movers of all
   const View& v = p.v;
   const int rank = blockIdx.x, ranks = gridDim.x, hk = blockIdx.y, b = blockIdx.z;
   const int warp = warp_id(), lane = lane_id(), tid = threadIdx.x;
@@ -90,23 +99,52 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectPara
   const int base = min(L, rank * per), mine = min(L - base, per);
   // 64 bits: next_pos - n_recent may pass the smallest int
   const long long recent = static_cast<long long>(p.next_pos[b]) - p.n_recent;
-  auto compute = [&](int i) -> uint32_t {
-    const int r = base + i;
-    const int page = page_at(v, b, page_entry(v, r));
-    if (page < 0) return 0u;
-    const size_t at = term_index(v, page, page_slot(v, r), hk);
-    const float w = p.weight[at];
-    return p.position[at] >= recent ? 0xFFFFFFFFu : weight_order(w);
-  };
+  auto order = [&](float w, int pos) { return pos >= recent ? 0xFFFFFFFFu : weight_order(w); };
   const int held = min(mine, p.smem_keys);
-#pragma unroll 4
-  for (int i = tid; i < held; i += kSelectThreads) s_key[i] = compute(i);
-  auto key = [&](int i) { return i < held ? s_key[i] : compute(i); };
+  constexpr int kBatch = 8;  // rows a thread has in flight: a page, then a weight and a position each
+  for (int i0 = tid; i0 < held; i0 += kBatch * kSelectThreads) {
+    int page[kBatch], pos[kBatch];
+    float w[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int i = i0 + j * kSelectThreads;
+      page[j] = i < held ? page_at(v, b, page_entry(v, base + i)) : -1;
+    }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      if (page[j] < 0) continue;
+      const size_t at = term_index(v, page[j], page_slot(v, base + i0 + j * kSelectThreads), hk);
+      w[j] = p.weight[at];
+      pos[j] = p.position[at];
+    }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int i = i0 + j * kSelectThreads;
+      if (i < held) s_key[i] = page[j] < 0 ? 0u : order(w[j], pos[j]);
+    }
+  }
+  auto key = [&](int i) -> uint32_t {
+    if (i < held) return s_key[i];
+    const int page = page_at(v, b, page_entry(v, base + i));
+    if (page < 0) return 0u;
+    const size_t at = term_index(v, page, page_slot(v, base + i), hk);
+    return order(p.weight[at], p.position[at]);
+  };
   __syncthreads();
 
+  // Of 32 values, the one that holds the want-th from the top (lane 31 first): its lane, and what is wanted of it.
+  auto pick = [&](uint32_t x, uint32_t want, int& at, uint32_t& rest) {
+    uint32_t inc = x;  // of this lane and those above
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t t = __shfl_down_sync(0xffffffffu, inc, o);
+      if (lane + o < 32) inc += t;
+    }
+    at = 31 - __clz(__ballot_sync(0xffffffffu, inc >= want));
+    rest = want - __shfl_sync(0xffffffffu, inc - x, at);
+  };
   // `want` keys are still to be found among those that start with `prefix`.
-  uint32_t prefix = 0u;
-  int want = p.n_keep;
+  uint32_t prefix = 0u, want = static_cast<uint32_t>(p.n_keep);
   for (int d = 0; d < 3; ++d) {
     const int shift = d == 0 ? 21 : (d == 1 ? 10 : 0);
     uint32_t* hist = s_hist[d & 1];
@@ -125,39 +163,44 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectPara
       if (lane == head_lane) atomicAdd(&hist[digit], __popc(same));
       else if (in && !((same >> lane) & 1u)) atomicAdd(&hist[digit], 1u);
     }
-    cluster_sync();
-    // Thread t holds bins 2t and 2t + 1 of all CTAs; suffix sums from the top.
-    // (each CTA starts with its own counts, so that not all read the same one)
-    uint32_t h0 = hist[2 * tid], h1 = hist[2 * tid + 1];
-#pragma unroll
-    for (int j = 1; j < kSelectMaxCluster; ++j) {
-      if (j >= ranks) break;
-      const uint2 h = peer_load2(&hist[2 * tid], (rank + j) % ranks);
-      h0 += h.x;
-      h1 += h.y;
-    }
-    uint32_t inc = h0 + h1;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t t = __shfl_down_sync(0xffffffffu, inc, o);
-      if (lane + o < 32) inc += t;
-    }
-    if (lane == 0) s_warp[warp] = inc;
     __syncthreads();
-    uint32_t later = s_warp[lane];  // of the warps behind this one
-    later = lane > warp ? later : 0u;
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) later += __shfl_xor_sync(0xffffffffu, later, o);
-    inc += later;
-    const uint32_t above = inc - h0 - h1;  // keys in bins over 2t + 1
-    if (above < static_cast<uint32_t>(want) && inc >= static_cast<uint32_t>(want)) {
-      const bool top = above + h1 >= static_cast<uint32_t>(want);
-      s_pick[0] = 2 * tid + (top ? 1 : 0);
-      s_pick[1] = static_cast<uint32_t>(want) - above - (top ? 0u : h1);
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t x = __reduce_add_sync(0xffffffffu, hist[(2 * warp + j) * 32 + lane]);
+      if (lane == 0) s_sum[d & 1][2 * warp + j] = x;
+    }
+    cluster_sync();
+    if (warp == 0) {
+      uint2 x = make_uint2(0u, 0u);  // sums 2 lane and 2 lane + 1 of all CTAs
+      uint32_t y = 0u;               // then a bin
+#pragma unroll
+      for (int j = 0; j < kSelectMaxCluster; ++j) {
+        if (j >= ranks) break;
+        const uint2 t = peer_load2(&s_sum[d & 1][2 * lane], (rank + j) % ranks);
+        x.x += t.x;
+        x.y += t.y;
+      }
+      int at, bin;
+      uint32_t rest;
+      pick(x.x + x.y, want, at, rest);
+      const uint32_t top = __shfl_sync(0xffffffffu, x.y, at);
+      const bool second = top >= rest;
+      at = 2 * at + (second ? 1 : 0);
+      if (!second) rest -= top;
+#pragma unroll
+      for (int j = 0; j < kSelectMaxCluster; ++j) {
+        if (j >= ranks) break;
+        y += peer_load(&hist[at * 32 + lane], (rank + j) % ranks);
+      }
+      pick(y, rest, bin, rest);
+      if (lane == 0) {
+        s_pick[0] = static_cast<uint32_t>(at * 32 + bin);
+        s_pick[1] = rest;
+      }
     }
     __syncthreads();
     prefix = d == 0 ? s_pick[0] : ((prefix << (d == 1 ? 11 : 10)) | s_pick[0]);
-    want = static_cast<int>(s_pick[1]);
+    want = s_pick[1];
     // The buffer of pass 0 serves pass 2: cleared here, while no CTA reads it
     // any more (all have passed the meeting of pass 1).
     if (d == 1) {
@@ -166,85 +209,105 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectPara
     }
   }
   // Kept: keys above `prefix`, and the first `want` rows equal to it. Each
-  // warp takes a run of consecutive rows and counts before it writes; a
-  // count's place is what the warps and the CTAs before it have.
+  // warp counts the ties and the larger keys of its run of rows, those below
+  // n_keep apart. Ties are taken in row order, so from these counts follow,
+  // for every warp and every CTA, the ties taken (want less the ties before),
+  // the holes and the movers, and where its own begin.
   const int seg = ((mine + 31) / 32 + 31) / 32 * 32;
   const int i_lo = min(mine, warp * seg), i_hi = min(mine, i_lo + seg);
-  auto before_warp = [&](uint32_t count, uint32_t& total) -> uint32_t {
-    __syncthreads();
-    if (lane == 0) s_warp[warp] = count;
-    __syncthreads();
-    const uint32_t x = s_warp[lane];
+  uint32_t c[4] = {0u, 0u, 0u, 0u};  // ties below n_keep, ties past it, larger below, larger past
+  for (int i0 = i_lo; i0 < i_hi; i0 += 32) {
+    const int i = i0 + lane;
+    const uint32_t k = i < i_hi ? key(i) : 0u;
+    const uint32_t tie = __ballot_sync(0xffffffffu, i < i_hi && k == prefix);
+    const uint32_t more = __ballot_sync(0xffffffffu, i < i_hi && k > prefix);
+    const uint32_t low = __ballot_sync(0xffffffffu, base + i < p.n_keep);
+    c[0] += __popc(tie & low);
+    c[1] += __popc(tie & ~low);
+    c[2] += __popc(more & low);
+    c[3] += __popc(more & ~low);
+  }
+  if (lane < 4) s_warp[lane][warp] = lane == 0 ? c[0] : (lane == 1 ? c[1] : (lane == 2 ? c[2] : c[3]));
+  __syncthreads();
+  // Holes and movers among `rows_low` rows below n_keep and those past it.
+  auto places = [&](uint32_t ties_before, uint32_t t_low, uint32_t t_high, uint32_t m_low, uint32_t m_high,
+                    uint32_t rows_low, uint32_t& holes, uint32_t& movers) {
+    const uint32_t taken = min(t_low + t_high, want - min(want, ties_before));
+    holes = rows_low - m_low - min(taken, t_low);
+    movers = m_high + (taken - min(taken, t_low));
+  };
+  auto rows_below = [&](int first, int last) {  // rows of [first, last) below n_keep
+    return static_cast<uint32_t>(max(0, min(last, p.n_keep) - min(first, p.n_keep)));
+  };
+  auto before_lane = [&](uint32_t x) {  // sum over the lanes before this one
     uint32_t inc = x;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += y;
+      const uint32_t t = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += t;
     }
-    total = __shfl_sync(0xffffffffu, inc, 31);
-    return __shfl_sync(0xffffffffu, inc - x, warp);
+    return inc - x;
   };
-  auto exchange = [&](int which) {  // the cluster's counts: lane k of warp 0 reads CTA k's
-    cluster_sync();
-    if (warp == 0) {
-      uint2 x = lane < ranks ? peer_load2(&s_count[which], lane) : make_uint2(0u, 0u);
-      uint2 b = lane < rank ? x : make_uint2(0u, 0u);
+  if (warp == 0) {
+    uint32_t t[4];
 #pragma unroll
-      for (int o = 16; o >= 1; o >>= 1) {
-        x.x += __shfl_xor_sync(0xffffffffu, x.x, o);
-        x.y += __shfl_xor_sync(0xffffffffu, x.y, o);
-        b.x += __shfl_xor_sync(0xffffffffu, b.x, o);
-        b.y += __shfl_xor_sync(0xffffffffu, b.y, o);
-      }
-      if (lane == 0) {
-        s_before = b;
-        s_all = x;
-      }
-    }
-    __syncthreads();
-  };
-  const uint32_t below = (1u << lane) - 1u;
-  uint32_t eq = 0u, cta_total;
-  for (int i0 = i_lo; i0 < i_hi; i0 += 32)
-    eq += __popc(__ballot_sync(0xffffffffu, i0 + lane < i_hi && key(i0 + lane) == prefix));
-  uint32_t eq_before = before_warp(eq, cta_total);
-  if (tid == 0) s_count[0] = make_uint2(cta_total, 0u);
-  exchange(0);
-  eq_before += s_before.x;
-  uint32_t hole_at = 0u, mover_at = 0u, total = 0u;
-  for (int pass = 0; pass < 2; ++pass) {
-    uint32_t e = eq_before, nh = hole_at, nm = mover_at;
-    for (int i0 = i_lo; i0 < i_hi; i0 += 32) {
-      const int i = i0 + lane, r = base + i;
-      const bool in = i < i_hi;
-      const uint32_t k = in ? key(i) : 0u;
-      const uint32_t tie = __ballot_sync(0xffffffffu, in && k == prefix);
-      const bool kept =
-          in && (k > prefix || (k == prefix && e + __popc(tie & below) < static_cast<uint32_t>(want)));
-      e += __popc(tie);
-      const bool hole = in && !kept && r < p.n_keep, mover = kept && r >= p.n_keep;
-      const uint32_t mh = __ballot_sync(0xffffffffu, hole), mm = __ballot_sync(0xffffffffu, mover);
-      if (pass == 1) {
-        if (hole) dst[nh + __popc(mh & below)] = r;
-        if (mover) src[nm + __popc(mm & below)] = r;
-      }
-      nh += __popc(mh);
-      nm += __popc(mm);
-    }
-    if (pass == 0) {
-      uint32_t cta_movers;
-      hole_at = before_warp(nh, cta_total);
-      mover_at = before_warp(nm, cta_movers);
-      if (tid == 0) s_count[1] = make_uint2(cta_total, cta_movers);
-      exchange(1);
-      hole_at += s_before.x;
-      mover_at += s_before.y;
-      total = s_all.y;
+    for (int j = 0; j < 4; ++j) t[j] = __reduce_add_sync(0xffffffffu, s_warp[j][lane]);
+    if (lane == 0) {
+      s_count[0] = make_uint2(t[0], t[1]);
+      s_count[1] = make_uint2(t[2], t[3]);
     }
   }
-  if (lead && tid == 0) p.n_moves[head] = static_cast<int>(total);
-  for (int i = static_cast<int>(total) + rank * kSelectThreads + tid; i < p.n_keep; i += ranks * kSelectThreads)
-    src[i] = dst[i] = -1;
+  cluster_sync();
+  if (warp == 0) {  // lane k: CTA k
+    uint2 ties = make_uint2(0u, 0u), more = make_uint2(0u, 0u);
+    uint32_t holes = 0u, movers = 0u;
+    if (lane < ranks) {
+      ties = peer_load2(&s_count[0], lane);
+      more = peer_load2(&s_count[1], lane);
+    }
+    const uint32_t ties_before = before_lane(ties.x + ties.y);
+    const int first = min(L, lane * per), last = min(L, first + per);
+    if (lane < ranks)
+      places(ties_before, ties.x, ties.y, more.x, more.y, rows_below(first, last), holes, movers);
+    const uint32_t holes_before = before_lane(holes), movers_before = before_lane(movers);
+    const uint32_t all = __reduce_add_sync(0xffffffffu, movers);
+    if (lane == rank) {
+      s_before[0] = ties_before;
+      s_before[1] = holes_before;
+      s_before[2] = movers_before;
+      s_total = all;
+    }
+  }
+  __syncthreads();
+  uint32_t e, nh, nm;  // ties, holes, movers before this warp's rows
+  {
+    const uint32_t t_low = s_warp[0][lane], t_high = s_warp[1][lane];  // lane k: warp k
+    const uint32_t ties_before = s_before[0] + before_lane(t_low + t_high);
+    const int first = base + min(mine, lane * seg), last = base + min(mine, (lane + 1) * seg);
+    uint32_t holes, movers;
+    places(ties_before, t_low, t_high, s_warp[2][lane], s_warp[3][lane], rows_below(first, last), holes, movers);
+    e = __shfl_sync(0xffffffffu, ties_before, warp);
+    nh = s_before[1] + __shfl_sync(0xffffffffu, before_lane(holes), warp);
+    nm = s_before[2] + __shfl_sync(0xffffffffu, before_lane(movers), warp);
+  }
+  const uint32_t below = (1u << lane) - 1u;
+  for (int i0 = i_lo; i0 < i_hi; i0 += 32) {
+    const int i = i0 + lane, r = base + i;
+    const bool in = i < i_hi;
+    const uint32_t k = in ? key(i) : 0u;
+    const uint32_t tie = __ballot_sync(0xffffffffu, in && k == prefix);
+    const bool kept = in && (k > prefix || (k == prefix && e + __popc(tie & below) < want));
+    e += __popc(tie);
+    const bool hole = in && !kept && r < p.n_keep, mover = kept && r >= p.n_keep;
+    const uint32_t mh = __ballot_sync(0xffffffffu, hole), mm = __ballot_sync(0xffffffffu, mover);
+    if (hole) dst[nh + __popc(mh & below)] = r;
+    if (mover) src[nm + __popc(mm & below)] = r;
+    nh += __popc(mh);
+    nm += __popc(mm);
+  }
+  const int total = static_cast<int>(s_total);
+  if (lead && tid == 0) p.n_moves[head] = total;
+  for (int i = total + rank * kSelectThreads + tid; i < p.n_keep; i += ranks * kSelectThreads) src[i] = dst[i] = -1;
   cluster_sync();  // no CTA leaves while another may still read its counts
 }
 
