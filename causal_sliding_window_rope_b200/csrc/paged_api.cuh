@@ -525,7 +525,7 @@ cswattn_status attn_paged_move(const cswattn_layer* layer, const cswattn_paged* 
   // At most min(n_keep, T - n_keep) rows move per head.
   const int most = std::min(n_keep, s.T - n_keep);
   if (most == 0) return CSWATTN_OK;
-  const int per = paged::kMoveThreads / (s.D / 8) * paged::kMoveBatch;
+  const int per = paged::kMoveThreads;
   const dim3 grid(std::min(paged::kMoveMaxCtas, (most + per - 1) / per), s.Hk, s.B);
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   {

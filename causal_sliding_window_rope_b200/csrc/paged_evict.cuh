@@ -320,73 +320,74 @@ struct MoveParams {
   int* position;
 };
 
-constexpr int kMoveThreads = 256;
-constexpr int kMoveMaxCtas = 256;    // of a head: its moves are spread over them
+constexpr int kMoveThreads = 256;    // moves of a CTA's step, too
+constexpr int kMoveMaxCtas = 64;     // of a head
 constexpr int kMoveBatch = 4;        // moves a group of lanes has in flight
 
-// D / 8 lanes copy one row of K and of V, 16 bytes each, kMoveBatch rows at a
-// time: the rows lie anywhere, so what counts is how many loads are in
-// flight behind the three dependent ones (move, page, row).
+// The rows lie anywhere, so what counts is how many loads are in flight. A
+// CTA takes kMoveThreads moves at a time: first a thread per move follows
+// move and page to the two rows' places (three dependent loads, paid once),
+// then D / 8 lanes copy a row of K and of V, kMoveBatch moves at a time.
 template <int D>
-__global__ void __launch_bounds__(kMoveThreads) move_kernel(const MoveParams p) {
+__global__ void __launch_bounds__(kMoveThreads, 4) move_kernel(const MoveParams p) {
   constexpr int LPR = D / 8, GPC = kMoveThreads / LPR;
+  __shared__ long long s_from[kMoveThreads], s_to[kMoveThreads];  // row of a pool of K or V rows; -1: none
   const View& v = p.v;
-  const int hk = blockIdx.y, b = blockIdx.z;
+  const int hk = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
   pdl_launch_dependents();
   pdl_wait();
   const size_t head = static_cast<size_t>(b) * v.Hk + hk;
   const int n = p.n_moves[head];
-  if (n < 0 || n > p.stride) {
-    if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&g_status, kStatusRange);
-    return;
-  }
-  const int sub = threadIdx.x % LPR;
-  for (int i0 = (blockIdx.x * GPC + threadIdx.x / LPR) * kMoveBatch; i0 < n; i0 += gridDim.x * GPC * kMoveBatch) {
-    int from[kMoveBatch], to[kMoveBatch], pf[kMoveBatch], pt[kMoveBatch];
-#pragma unroll
-    for (int j = 0; j < kMoveBatch; ++j) {
-      const bool in = i0 + j < n;
-      from[j] = in ? p.src[head * p.stride + i0 + j] : 0;
-      to[j] = in ? p.dst[head * p.stride + i0 + j] : 0;
+  for (int i0 = blockIdx.x * kMoveThreads; i0 < p.stride; i0 += gridDim.x * kMoveThreads) {
+    const bool in = i0 + tid < p.stride;
+    const int from = in ? p.src[head * p.stride + i0 + tid] : 0;  // (beside n: one latency less)
+    const int to = in ? p.dst[head * p.stride + i0 + tid] : 0;
+    if (n < 0 || n > p.stride) {
+      if (blockIdx.x == 0 && tid == 0) atomicOr(&g_status, kStatusRange);
+      return;
     }
-#pragma unroll
-    for (int j = 0; j < kMoveBatch; ++j) {
-      pf[j] = pt[j] = -1;
-      if (i0 + j >= n) continue;
-      if (from[j] < 0 || from[j] >= v.T || to[j] < 0 || to[j] >= v.T) {
+    if (i0 >= n) return;
+    long long a = -1, z = -1;
+    if (i0 + tid < n) {
+      if (from < 0 || from >= v.T || to < 0 || to >= v.T) {
         atomicOr(&g_status, kStatusRange);
-        continue;
+      } else {
+        const int pf = page_at(v, b, page_entry(v, from)), pt = page_at(v, b, page_entry(v, to));
+        if (pf >= 0 && pt >= 0) {
+          a = static_cast<long long>(kv_index(v, pf, page_slot(v, from), hk));
+          z = static_cast<long long>(kv_index(v, pt, page_slot(v, to), hk));
+          const size_t ta = term_index(v, pf, page_slot(v, from), hk), tz = term_index(v, pt, page_slot(v, to), hk);
+          const float w = p.weight[ta];
+          const int pos = p.position[ta];
+          p.weight[tz] = w;
+          p.position[tz] = pos;
+        }
       }
-      pf[j] = page_at(v, b, page_entry(v, from[j]));
-      pt[j] = page_at(v, b, page_entry(v, to[j]));
     }
-    uint4 kk[kMoveBatch], vv[kMoveBatch];
-    float w[kMoveBatch];
-    int pos[kMoveBatch];
+    s_from[tid] = a;
+    s_to[tid] = z;
+    __syncthreads();
+    const int count = min(n - i0, kMoveThreads), sub = tid % LPR;
+    for (int m0 = tid / LPR; m0 < count; m0 += GPC * kMoveBatch) {
+      uint4 kk[kMoveBatch], vv[kMoveBatch];
 #pragma unroll
-    for (int j = 0; j < kMoveBatch; ++j) {
-      if (pf[j] < 0 || pt[j] < 0) continue;
-      const int slot = page_slot(v, from[j]);
-      const size_t a = kv_index(v, pf[j], slot, hk) * D + sub * 8;
-      kk[j] = *reinterpret_cast<const uint4*>(p.k_pages + a);
-      vv[j] = *reinterpret_cast<const uint4*>(p.v_pages + a);
-      if (sub == 0) {
-        w[j] = p.weight[term_index(v, pf[j], slot, hk)];
-        pos[j] = p.position[term_index(v, pf[j], slot, hk)];
+      for (int j = 0; j < kMoveBatch; ++j) {
+        const int m = m0 + j * GPC;
+        if (m >= count || s_from[m] < 0) continue;
+        const size_t at = static_cast<size_t>(s_from[m]) * D + sub * 8;
+        kk[j] = *reinterpret_cast<const uint4*>(p.k_pages + at);
+        vv[j] = *reinterpret_cast<const uint4*>(p.v_pages + at);
       }
-    }
 #pragma unroll
-    for (int j = 0; j < kMoveBatch; ++j) {
-      if (pf[j] < 0 || pt[j] < 0) continue;
-      const int slot = page_slot(v, to[j]);
-      const size_t z = kv_index(v, pt[j], slot, hk) * D + sub * 8;
-      *reinterpret_cast<uint4*>(p.k_pages + z) = kk[j];
-      *reinterpret_cast<uint4*>(p.v_pages + z) = vv[j];
-      if (sub == 0) {
-        p.weight[term_index(v, pt[j], slot, hk)] = w[j];
-        p.position[term_index(v, pt[j], slot, hk)] = pos[j];
+      for (int j = 0; j < kMoveBatch; ++j) {
+        const int m = m0 + j * GPC;
+        if (m >= count || s_from[m] < 0) continue;
+        const size_t at = static_cast<size_t>(s_to[m]) * D + sub * 8;
+        *reinterpret_cast<uint4*>(p.k_pages + at) = kk[j];
+        *reinterpret_cast<uint4*>(p.v_pages + at) = vv[j];
       }
     }
+    __syncthreads();
   }
 }
 
