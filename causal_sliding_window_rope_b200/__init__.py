@@ -310,29 +310,41 @@ def attn_decode(spec: LayerSpec, q, k, v, ve, gate, cache_len, k_cache, v_cache,
 # ------------------------------------------------------------------ paged cache
 
 @functools.lru_cache(maxsize=64)
-def _rope_frequencies(R, scaling, factor, base, original_length, beta_fast, beta_slow):
-    """(frequencies, factor on cos and sin) of RopeSpec's scalings."""
+def _rope(R, interleaved, scaling, factor, base, original_length, beta_fast, beta_slow, attention_factor, frequencies):
+    """(frequencies, factor on cos and sin, C struct) of a RopeSpec."""
+    if R < 2 or R % 2:
+        raise ValueError(f"rotary_dim must be even and >= 2, got {R}")
+    if scaling not in RopeSpec.SCALINGS:
+        raise ValueError(f"scaling must be one of {RopeSpec.SCALINGS}, got {scaling!r}")
+    if not (math.isfinite(factor) and factor > 0) or not (math.isfinite(base) and base > 0):
+        raise ValueError("factor and base must be finite and > 0")
     scale = 1.0
-    if scaling == "ntk":
-        if R == 2:
-            raise ValueError("ntk scaling needs rotary_dim > 2")
-        base = base * factor ** (R / (R - 2))
-    w = [base ** (-2.0 * i / R) for i in range(R // 2)]
-    if scaling == "linear":
-        w = [f / factor for f in w]
-    elif scaling == "yarn":
-        if not original_length or base == 1.0:
-            raise ValueError("yarn scaling needs original_length and a base other than 1")
+    if frequencies is not None:
+        w = list(frequencies)
+        if len(w) != R // 2:
+            raise ValueError(f"{R // 2} frequencies are wanted, got {len(w)}")
+    else:
+        if scaling == "ntk":
+            if R == 2:
+                raise ValueError("ntk scaling needs rotary_dim > 2")
+            base = base * factor ** (R / (R - 2))
+        w = [base ** (-2.0 * i / R) for i in range(R // 2)]
+        if scaling == "linear":
+            w = [f / factor for f in w]
+        elif scaling == "yarn":
+            if not original_length or base == 1.0:
+                raise ValueError("yarn scaling needs original_length and a base other than 1")
 
-        def pair_of(turns):  # the pair that turns this often within original_length
-            return R * math.log(original_length / (turns * 2 * math.pi)) / (2 * math.log(base))
-        low = max(math.floor(pair_of(beta_fast)), 0)
-        high = min(math.ceil(pair_of(beta_slow)), R // 2 - 1)
-        for i in range(R // 2):
-            ramp = min(max((i - low) / max(high - low, 0.001), 0.0), 1.0)
-            w[i] = w[i] * (1 - ramp) + w[i] / factor * ramp
-        scale = 0.1 * math.log(factor) + 1.0
-    return tuple(w), scale, (ctypes.c_double * len(w))(*w)
+            def pair_of(turns):  # the pair that turns this often within original_length
+                return R * math.log(original_length / (turns * 2 * math.pi)) / (2 * math.log(base))
+            low = max(math.floor(pair_of(beta_fast)), 0)
+            high = min(math.ceil(pair_of(beta_slow)), R // 2 - 1)
+            for i in range(R // 2):
+                ramp = min(max((i - low) / max(high - low, 0.001), 0.0), 1.0)
+                w[i] = w[i] * (1 - ramp) + w[i] / factor * ramp
+            scale = 0.1 * math.log(factor) + 1.0
+    scale = float(scale if attention_factor is None else attention_factor)
+    return tuple(w), scale, CswattnRope(R, int(interleaved), scale, (ctypes.c_double * len(w))(*w))
 
 
 class RopeSpec:
@@ -356,23 +368,12 @@ class RopeSpec:
 
     def __init__(self, rotary_dim, interleaved=False, scaling="none", factor=1.0, base=10000.0,
                  original_length=None, beta_fast=32.0, beta_slow=1.0, attention_factor=None, frequencies=None):
-        R = int(rotary_dim)
-        if R < 2 or R % 2:
-            raise ValueError(f"rotary_dim must be even and >= 2, got {rotary_dim}")
-        if scaling not in self.SCALINGS:
-            raise ValueError(f"scaling must be one of {self.SCALINGS}, got {scaling!r}")
-        if not (math.isfinite(factor) and factor > 0) or not (math.isfinite(base) and base > 0):
-            raise ValueError("factor and base must be finite and > 0")
+        self.rotary_dim, self.interleaved = int(rotary_dim), bool(interleaved)
         if frequencies is not None:
-            w, scale = tuple(float(f) for f in frequencies), 1.0
-            if len(w) != R // 2:
-                raise ValueError(f"{R // 2} frequencies are wanted, got {len(w)}")
-            array = (ctypes.c_double * len(w))(*w)
-        else:
-            w, scale, array = _rope_frequencies(R, scaling, factor, base, original_length, beta_fast, beta_slow)
-        self.rotary_dim, self.interleaved, self.frequencies = R, bool(interleaved), w
-        self.attention_factor = float(scale if attention_factor is None else attention_factor)
-        self._c = CswattnRope(R, int(self.interleaved), self.attention_factor, array)
+            frequencies = tuple(float(f) for f in frequencies)
+        self.frequencies, self.attention_factor, self._c = _rope(
+            self.rotary_dim, self.interleaved, scaling, factor, base, original_length, beta_fast, beta_slow,
+            attention_factor, frequencies)
 
 
 def _want(device, *tensors):

@@ -77,9 +77,9 @@ __global__ void __launch_bounds__(32 * (4 * WeighGroups<NT>::value + 1), 1)
   }
   pdl_wait();
   fill_prefix(v, pre, p.max_rows, c == 0);
-  const Deal deal(static_cast<long long>(pre[v.B]) * v.Hk, gridDim.x);
+  const Deal deal(v, pre, gridDim.x);
   if (c >= deal.ctas) return;
-  Walk w(pre, v.B, v.Hk, deal.begin(c), deal.begin(c + 1));
+  Walk w(deal, c);
   const WaitCtx wc{abort_flag, p.wait_ns};
 
   if (warp == kWarps) {
