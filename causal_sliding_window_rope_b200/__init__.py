@@ -311,7 +311,7 @@ def attn_decode(spec: LayerSpec, q, k, v, ve, gate, cache_len, k_cache, v_cache,
 
 @functools.lru_cache(maxsize=64)
 def _rope(R, interleaved, scaling, factor, base, original_length, beta_fast, beta_slow, attention_factor, frequencies):
-    """(frequencies, factor on cos and sin, C struct) of a RopeSpec."""
+    """(frequencies, factor on cos and sin, C struct, its address) of a RopeSpec."""
     if R < 2 or R % 2:
         raise ValueError(f"rotary_dim must be even and >= 2, got {R}")
     if scaling not in RopeSpec.SCALINGS:
@@ -344,7 +344,8 @@ def _rope(R, interleaved, scaling, factor, base, original_length, beta_fast, bet
                 w[i] = w[i] * (1 - ramp) + w[i] / factor * ramp
             scale = 0.1 * math.log(factor) + 1.0
     scale = float(scale if attention_factor is None else attention_factor)
-    return tuple(w), scale, CswattnRope(R, int(interleaved), scale, (ctypes.c_double * len(w))(*w))
+    struct = CswattnRope(R, int(interleaved), scale, (ctypes.c_double * len(w))(*w))
+    return tuple(w), scale, struct, ctypes.addressof(struct)
 
 
 class RopeSpec:
@@ -371,31 +372,31 @@ class RopeSpec:
         self.rotary_dim, self.interleaved = int(rotary_dim), bool(interleaved)
         if frequencies is not None:
             frequencies = tuple(float(f) for f in frequencies)
-        self.frequencies, self.attention_factor, self._c = _rope(
+        self.frequencies, self.attention_factor, self._c, self.address = _rope(
             self.rotary_dim, self.interleaved, scaling, factor, base, original_length, beta_fast, beta_slow,
             attention_factor, frequencies)
 
 
-def _want(device, *tensors):
-    """Each (name, tensor, shape, dtype): a contiguous CUDA tensor of that
-    shape and type on the device of this index."""
-    for name, t, shape, dtype in tensors:
-        if t is None:
-            raise ValueError(f"{name} is needed")
-        if t.dtype is not dtype or t.shape != shape or t.get_device() != device or device < 0 or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape {tuple(shape)} on the device of "
-                             f"the call's others, got {t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}")
+_paged = None
 
 
-@functools.lru_cache(maxsize=256)
-def _layer_struct(*fields):
-    return ctypes.byref(LayerSpec(*fields).c())
-
-
-def _layer_ref(s: LayerSpec):
-    """The C struct of a layer, for calls that do not write to it."""
-    return _layer_struct(s.B, s.T, s.n_head, s.n_kv_head, s.head_dim, s.window, s.has_ve, s.dtype, s.rope_base, s.eps,
-                         s.softmax_scale)
+def _paged_calls():
+    """The module that checks and makes the paged calls, bound to the loaded
+    library. Raises if it has not been built: there is no fallback."""
+    global _paged
+    if _paged is None:
+        import torch  # noqa: F401  (the module is linked against its libraries)
+        try:
+            from . import _paged_binding as m
+        except ImportError as e:
+            raise RuntimeError("_paged_binding.so is missing or does not fit this PyTorch; build it with "
+                               "`python -m causal_sliding_window_rope_b200.build`") from e
+        L = lib()
+        m.bind(CswattnError, *(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            L.attn_paged_append, L.attn_paged, L.attn_paged_weigh, L.attn_paged_select, L.attn_paged_move,
+            L.cswattn_last_error)))
+        _paged = m
+    return _paged
 
 
 class PagedCache:
@@ -414,36 +415,9 @@ class PagedCache:
             if track_weights:
                 weight = torch.zeros(*term, device=device) if weight is None else weight
                 position = torch.zeros(*term, device=device, dtype=torch.int32) if position is None else position
-        if k is not None:
-            n_pages, page_size = k.shape[0], k.shape[1]
-            self.device = k.get_device()
-        elif weight is not None:
-            n_pages, page_size = weight.shape[0], weight.shape[2]
-            self.device = weight.get_device()
-        else:
-            raise ValueError("PagedCache needs n_pages and page_size, or the pools")
-        self.heads = heads = (spec.n_kv_head, spec.head_dim)
-        if k is not None:
-            _want(self.device, ("k", k, (n_pages, page_size) + heads, torch.bfloat16))
-        if v is not None:
-            _want(self.device, ("v", v, (n_pages, page_size) + heads, torch.bfloat16))
-        if weight is not None:
-            _want(self.device, ("weight", weight, (n_pages, heads[0], page_size), torch.float32))
-        if position is not None:
-            _want(self.device, ("position", position, (n_pages, heads[0], page_size), torch.int32))
+        self.n_pages, self.page_size = (_paged or _paged_calls()).check_cache(spec.n_kv_head, spec.head_dim, k, v,
+                                                                              weight, position)
         self.k, self.v, self.weight, self.position = k, v, weight, position
-        self.n_pages, self.page_size = n_pages, page_size
-
-    def need(self, spec: LayerSpec, device, *pools):
-        """Checks that these (of its) pools are there, for a call of `spec` on `device`."""
-        if self.heads[0] != spec.n_kv_head or self.heads[1] != spec.head_dim:
-            raise ValueError(f"the cache holds (n_kv_head, head_dim) = {self.heads}, the layer "
-                             f"{(spec.n_kv_head, spec.head_dim)}")
-        if self.device != device:
-            raise ValueError(f"the cache lies on cuda:{self.device}, the batch on cuda:{device}")
-        for t in pools:
-            if t is None:
-                raise ValueError("the cache lacks a pool that the call needs (k, v; weight, position: track_weights)")
 
 
 class PagedBatch:
@@ -453,142 +427,66 @@ class PagedBatch:
     not needed to select and move rows)."""
 
     def __init__(self, page_table, cache_len, new_start=None, n_tokens=0, max_new=0):
-        import torch
-        B, pages = page_table.shape
-        self.device = page_table.get_device()
-        _want(self.device, ("page_table", page_table, (B, pages), torch.int32), ("cache_len", cache_len, (B,), torch.int32))
-        if new_start is not None:
-            _want(self.device, ("new_start", new_start, (B + 1,), torch.int32))
+        (_paged or _paged_calls()).check_batch(page_table, cache_len, new_start)
         self.page_table, self.cache_len, self.new_start = page_table, cache_len, new_start
-        self.n_tokens, self.max_new = int(n_tokens), int(max_new)
+        self.n_tokens, self.max_new = n_tokens, max_new
 
-    def c(self, spec: LayerSpec, cache: PagedCache) -> CswattnPaged:
-        B, pages = self.page_table.shape
-        if B != spec.B:
-            raise ValueError(f"the batch has {B} sequences, the layer {spec.B}")
-        start = self.new_start
-        return CswattnPaged(cache.page_size, cache.n_pages, pages, self.n_tokens, self.max_new,
+    def c(self, cache: PagedCache) -> CswattnPaged:
+        return CswattnPaged(cache.page_size, cache.n_pages, self.page_table.shape[1], self.n_tokens, self.max_new,
                             self.page_table.data_ptr(), self.cache_len.data_ptr(),
-                            None if start is None else start.data_ptr())
-
-
-def _paged_call(fn, device, stream, *args):
-    """Calls an entry point with the tensors' device current (the kernels run
-    in its context) on the stream given, or on that device's current one."""
-    import torch
-    if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(device)
-    elif not isinstance(stream, int):
-        stream = stream.cuda_stream
-    if torch._C._cuda_getDevice() == device:
-        status = fn(*args, stream)
-    else:
-        with torch.cuda.device(device):
-            status = fn(*args, stream)
-    if status != OK:
-        _check(status)
-
-
-def _at(t):
-    return None if t is None else t.data_ptr()
+                            None if self.new_start is None else self.new_start.data_ptr())
 
 
 def attn_paged_append(spec: LayerSpec, batch: PagedBatch, cache: PagedCache, q, k, v, ve, gate, q_out,
                       positions=None, rope: RopeSpec | None = None, stream=None):
     """The prologue of the batch's new tokens: q_out, and their rows of the
     cache. rope None: the layer's plain RoPE."""
-    import torch
-    N, H, Hk, D, dev = batch.n_tokens, spec.n_head, spec.n_kv_head, spec.head_dim, batch.device
-    bf, qs, ks = torch.bfloat16, (N, H, D), (N, Hk, D)
-    _want(dev, ("q", q, qs, bf), ("k", k, ks, bf), ("v", v, ks, bf), ("q_out", q_out, qs, bf))
-    if spec.has_ve:
-        _want(dev, ("ve", ve, ks, bf), ("gate", gate, (N, Hk), bf))
-    if positions is not None:
-        _want(dev, ("positions", positions, (N,), torch.int32))
-    cache.need(spec, dev, cache.k, cache.v)
-    _paged_call(lib().attn_paged_append, dev, stream, _layer_ref(spec), ctypes.byref(batch.c(spec, cache)),
-                None if rope is None else ctypes.byref(rope._c), q.data_ptr(), k.data_ptr(), v.data_ptr(), _at(ve),
-                _at(gate), _at(positions), q_out.data_ptr(), cache.k.data_ptr(), cache.v.data_ptr(),
-                _at(cache.weight), _at(cache.position))
+    (_paged or _paged_calls()).append(spec, batch, cache, q, k, v, ve, gate, q_out, positions, rope, stream)
 
 
 def attn_paged_workspace_bytes(spec: LayerSpec, batch: PagedBatch, cache: PagedCache) -> int:
     """Scratch bytes of attn_paged for this layer and the batch's sizes."""
-    return int(lib().attn_paged_workspace_bytes(_layer_ref(spec), ctypes.byref(batch.c(spec, cache))))
+    return int(lib().attn_paged_workspace_bytes(ctypes.byref(spec.c()), ctypes.byref(batch.c(cache))))
 
 
 def attn_paged(spec: LayerSpec, batch: PagedBatch, cache: PagedCache, q_out, O, lse, workspace,
                workspace_bytes=None, stream=None):
     """Attention of the new tokens (q_out of attn_paged_append) over the
     cache: O (n_tokens, H, D) and lse (n_tokens, H)."""
-    import torch
-    N, H, D, dev = batch.n_tokens, spec.n_head, spec.head_dim, batch.device
-    bf, qs = torch.bfloat16, (N, H, D)
-    _want(dev, ("q_out", q_out, qs, bf), ("O", O, qs, bf), ("lse", lse, (N, H), torch.float32),
-          ("workspace", workspace, workspace.shape, workspace.dtype))
-    if workspace_bytes is None:
-        workspace_bytes = workspace.numel() * workspace.element_size()
-    cache.need(spec, dev, cache.k, cache.v)
-    _paged_call(lib().attn_paged, dev, stream, _layer_ref(spec), ctypes.byref(batch.c(spec, cache)),
-                q_out.data_ptr(), cache.k.data_ptr(), cache.v.data_ptr(), O.data_ptr(), lse.data_ptr(),
-                workspace.data_ptr(), workspace_bytes)
+    (_paged or _paged_calls()).attend(spec, batch, cache, q_out, O, lse, workspace, workspace_bytes, stream)
 
 
 def attn_paged_weigh_workspace_bytes(spec: LayerSpec, batch: PagedBatch, cache: PagedCache) -> int:
     """Scratch bytes of attn_paged_weigh; 0 for a call of few query rows."""
-    return int(lib().attn_paged_weigh_workspace_bytes(_layer_ref(spec), ctypes.byref(batch.c(spec, cache))))
+    return int(lib().attn_paged_weigh_workspace_bytes(ctypes.byref(spec.c()), ctypes.byref(batch.c(cache))))
 
 
 def attn_paged_weigh(spec: LayerSpec, batch: PagedBatch, cache: PagedCache, q_out, lse, workspace=None, stream=None):
     """Adds the new tokens' attention weights to cache.weight. workspace:
     attn_paged_weigh_workspace_bytes of scratch; None: a call that needs some
     takes it from PyTorch's allocator on its stream."""
-    import torch
-    N, H, dev = batch.n_tokens, spec.n_head, batch.device
-    _want(dev, ("q_out", q_out, (N, H, spec.head_dim), torch.bfloat16), ("lse", lse, (N, H), torch.float32))
-    cache.need(spec, dev, cache.k, cache.weight)
-    layer, paged = _layer_ref(spec), ctypes.byref(batch.c(spec, cache))
-    if workspace is not None:
-        _want(dev, ("workspace", workspace, workspace.shape, workspace.dtype))
-    elif batch.max_new * H > 8 * spec.n_kv_head:  # else none is needed, whatever the sizes
-        nbytes = int(lib().attn_paged_weigh_workspace_bytes(layer, paged))
-        if nbytes:
-            if stream is None:
-                workspace = torch.empty(nbytes, dtype=torch.uint8, device=batch.page_table.device)
-            else:
-                s = torch.cuda.ExternalStream(stream, dev) if isinstance(stream, int) else stream
-                with torch.cuda.stream(s):  # freed memory is reused in this stream's order
-                    workspace = torch.empty(nbytes, dtype=torch.uint8, device=batch.page_table.device)
-    _paged_call(lib().attn_paged_weigh, dev, stream, layer, paged, q_out.data_ptr(), cache.k.data_ptr(),
-                lse.data_ptr(), cache.weight.data_ptr(), _at(workspace),
-                0 if workspace is None else workspace.numel() * workspace.element_size())
+    if workspace is None and batch.max_new * spec.n_head > 32 * spec.n_kv_head:  # fewer query rows need none
+        import torch
+        nbytes, device = attn_paged_weigh_workspace_bytes(spec, batch, cache), batch.page_table.device
+        if stream is None:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        else:
+            s = torch.cuda.ExternalStream(stream, device) if isinstance(stream, int) else stream
+            with torch.cuda.stream(s):  # freed memory is reused in this stream's order
+                workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    (_paged or _paged_calls()).weigh(spec, batch, cache, q_out, lse, workspace, stream)
 
 
 def attn_paged_select(spec: LayerSpec, batch: PagedBatch, cache: PagedCache, next_pos, n_keep, n_recent, n_moves,
                       src, dst, new_len, stream=None):
     """Which rows each KV head keeps under a budget of n_keep rows, as moves
     (src, dst) of n_moves rows, and the sequences' new lengths."""
-    import torch
-    B, Hk, dev = spec.B, spec.n_kv_head, batch.device
-    i32, ms = torch.int32, (B, Hk, n_keep)
-    _want(dev, ("next_pos", next_pos, (B,), i32), ("n_moves", n_moves, (B, Hk), i32), ("src", src, ms, i32),
-          ("dst", dst, ms, i32), ("new_len", new_len, (B,), i32))
-    cache.need(spec, dev, cache.weight, cache.position)
-    _paged_call(lib().attn_paged_select, dev, stream, _layer_ref(spec), ctypes.byref(batch.c(spec, cache)),
-                cache.weight.data_ptr(), cache.position.data_ptr(), next_pos.data_ptr(), n_keep, n_recent,
-                n_moves.data_ptr(), src.data_ptr(), dst.data_ptr(), new_len.data_ptr())
+    (_paged or _paged_calls()).select(spec, batch, cache, next_pos, n_keep, n_recent, n_moves, src, dst, new_len, stream)
 
 
 def attn_paged_move(spec: LayerSpec, batch: PagedBatch, cache: PagedCache, n_moves, src, dst, stream=None):
     """Moves the kept rows of attn_paged_select to their new places."""
-    import torch
-    B, Hk, n_keep, dev = spec.B, spec.n_kv_head, src.shape[-1], batch.device
-    i32, ms = torch.int32, (B, Hk, n_keep)
-    _want(dev, ("n_moves", n_moves, (B, Hk), i32), ("src", src, ms, i32), ("dst", dst, ms, i32))
-    cache.need(spec, dev, cache.k, cache.v, cache.weight, cache.position)
-    _paged_call(lib().attn_paged_move, dev, stream, _layer_ref(spec), ctypes.byref(batch.c(spec, cache)),
-                n_moves.data_ptr(), src.data_ptr(), dst.data_ptr(), n_keep,
-                cache.k.data_ptr(), cache.v.data_ptr(), cache.weight.data_ptr(), cache.position.data_ptr())
+    (_paged or _paged_calls()).move(spec, batch, cache, n_moves, src, dst, stream)
 
 
 def cswattn_sync_status(stream=None):

@@ -18,7 +18,9 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libcswattn.so")
 LIB_CHECK = os.path.join(PKG, "libcswattn_check.so")  # CSWATTN_CHECK=1: device-side bounds checks
+LIB_BINDING = os.path.join(PKG, "_paged_binding.so")  # Python module: checks and makes the paged cache's calls
 SOURCES = ["cswattn.cu"]
+BINDING_SOURCE = os.path.join(CSRC, "paged_binding.cpp")
 HEADER = os.path.join(ROOT, "include", "cswattn.h")
 
 
@@ -49,12 +51,40 @@ def stale(lib: str | None = None) -> bool:
     if not os.path.exists(lib):
         return True
     t = os.path.getmtime(lib)
-    return any(os.path.getmtime(d) > t for d in deps())
+    return any(os.path.getmtime(d) > t for d in (binding_deps() if lib == LIB_BINDING else deps()))
+
+
+def binding_deps() -> list[str]:
+    return [BINDING_SOURCE, HEADER, os.path.abspath(__file__)]
+
+
+def build_binding(force: bool = False) -> str:
+    """Compile the Python module _paged_binding (host code only, against the
+    installed Python's and PyTorch's headers)."""
+    if not force and not stale(LIB_BINDING):
+        return LIB_BINDING
+    import sysconfig
+
+    import torch
+    base = os.path.join(os.path.dirname(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(nvcc())) if os.path.isabs(nvcc()) else "/usr/local/cuda"
+    tmp = LIB_BINDING + f".tmp{os.getpid()}"
+    subprocess.check_call([
+        os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+        f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+        "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(base, "include"),
+        "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+        "-isystem", os.path.join(cuda, "include"), BINDING_SOURCE, "-o", tmp,
+        "-L", os.path.join(base, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"])
+    os.replace(tmp, LIB_BINDING)
+    return LIB_BINDING
 
 
 def build(force: bool = False, verbose: bool = False, check: bool = False) -> str:
     """Compile libcswattn.so (or, with check, libcswattn_check.so: the same
-    library with CSWATTN_CHECK=1 device-side bounds checks)."""
+    library with CSWATTN_CHECK=1 device-side bounds checks), and the Python
+    module that makes the paged cache's calls."""
+    build_binding(force)
     lib = LIB_CHECK if check else LIB
     if not force and not stale(lib):
         return lib

@@ -523,7 +523,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const JoinParams 
   pdl_launch_dependents();
   pdl_wait();
   const View& v = p.v;
-  Seq s;
+  Seq s{};
   auto out_row = [&](int hk, int i, int h) { return static_cast<size_t>(s.tok0 + i) * v.H + hk * v.g + h; };
   const int pairs = v.B * v.Hk;
   if (static_cast<int>(blockIdx.x) < pairs) {
