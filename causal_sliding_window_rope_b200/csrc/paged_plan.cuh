@@ -15,6 +15,14 @@ constexpr int kSMs = 148;
 constexpr int kMaxRuns = 2 * kSMs;  // CTAs that work may be dealt to
 constexpr int kPlanMinBlocks = 2;   // fewest blocks worth a CTA of their own
 
+// total c / n, in 32 bits where they hold the product (a 64-bit division costs
+// a few hundred cycles, and a CTA's start is a tenth of a generation step).
+static_assert(kMaxRuns < 512, "share_of in 32 bits");
+__device__ __forceinline__ long long share_of(long long total, int c, int n) {
+  if (total < (1 << 23)) return static_cast<uint32_t>(total) * static_cast<uint32_t>(c) / static_cast<uint32_t>(n);
+  return total * c / n;
+}
+
 // Where a CTA's run starts: the k-th long sequence, KV head, unit, block of the unit.
 struct Start {
   int k, hk, unit, t0;
@@ -147,7 +155,7 @@ __device__ __forceinline__ void find_run(const View& v, const Units& units, int 
     const int ctas = static_cast<int>(most < runs ? most : runs);
     if (c == 0 && lane == 0) plan->ctas = ctas;
     if (c < ctas) {
-      const long long at = total * c / ctas;
+      const long long at = share_of(total, c, ctas);
       int lo = 0, hi = n_long;  // the last k with pre[k] * Hk <= at
       while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
@@ -173,7 +181,7 @@ __device__ __forceinline__ void find_run(const View& v, const Units& units, int 
           const Start st{lo, static_cast<int>(rem / cnt), u, static_cast<int>(left) - (inc - mine)};
           plan->start[c] = st;
           run->st = st;
-          run->left = total * (c + 1) / ctas - at;
+          run->left = share_of(total, c + 1, ctas) - at;
         }
         if (__any_sync(0xffffffffu, here)) break;
         left -= __shfl_sync(0xffffffffu, inc, 31);

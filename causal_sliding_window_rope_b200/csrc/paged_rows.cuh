@@ -79,47 +79,80 @@ struct Deal {
   int B, Hk;
   long long total;
   int ctas;
-  bool whole = false;
-  __device__ Deal(const View& v, const int* pre_, int grid)
-      : pre(pre_), B(v.B), Hk(v.Hk), total(static_cast<long long>(pre_[v.B]) * v.Hk) {
-    const long long most = (total + kMinBlocks - 1) / kMinBlocks;
-    ctas = static_cast<int>(most < grid ? most : grid);
+  bool whole;
+  long long at, end;  // this CTA's run
+  int b;              // the sequence that holds its first block
+
+  __device__ int owner(long long x) const {
+    return total < (1 << 23) ? static_cast<int>((static_cast<uint32_t>(x + 1) * ctas - 1) / static_cast<uint32_t>(total))
+                             : static_cast<int>(((x + 1) * ctas - 1) / total);
   }
-  // The sequence that holds block x: the last b with pre[b] * Hk <= x.
+  // The last b with pre[b] * Hk <= x.
   __device__ int sequence(long long x) const {
+    const int y = total < (1 << 23) ? static_cast<int>(static_cast<uint32_t>(x) / static_cast<uint32_t>(Hk))
+                                    : static_cast<int>(x / Hk);
     int lo = 0, hi = B;
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
-      if (static_cast<long long>(pre[mid]) * Hk <= x) lo = mid;
+      if (pre[mid] <= y) lo = mid;
       else hi = mid;
     }
     return lo;
   }
-  __device__ long long begin(int c) const {
-    const long long x = total * c / ctas;
-    if (!whole || c == ctas) return x;
-    const int b = sequence(x), cnt = pre[b + 1] - pre[b];
-    const long long at = static_cast<long long>(pre[b]) * Hk;
-    return at + (x - at + cnt - 1) / cnt * cnt;
-  }
-  __device__ int owner(long long x) const { return static_cast<int>(((x + 1) * ctas - 1) / total); }
-  // Whole pairs, where no CTA's run then exceeds the average by a quarter: the
-  // SMs share HBM, so the others' runs are read no slower, and nothing is left
-  // to join (32 sequences of 2048 rows on 4 KV heads, 128 pairs: 31.0 -> 29.8 us;
-  // runs twice the average would leave most SMs idle behind the others).
-  // All threads of the CTA call; `longest` is in shared memory.
-  __device__ void settle(int* longest) {
-    if (threadIdx.x == 0) *longest = 0;
-    __syncthreads();
-    whole = true;
-    for (int c = threadIdx.x; c < ctas; c += blockDim.x) {
-      const long long run = begin(c + 1) - begin(c);
-      atomicMax(longest, run < (1 << 30) ? static_cast<int>(run) : (1 << 30));
-    }
-    __syncthreads();
-    whole = 4ll * *longest * ctas <= 5 * total;
-  }
 };
+
+struct DealShared {
+  long long begin[kSMs + 1], pair[kSMs + 1];  // of each run: its block, and the first pair that begins there or later
+  int b[kSMs + 1], pair_b[kSMs + 1];
+};
+
+// All threads call (at least as many as CTAs). With may_be_whole, whole pairs
+// where no run then exceeds the average by a quarter: the SMs share HBM, so
+// the others' runs are read no slower, and nothing is left to join
+// (32 sequences of 2048 rows on 4 KV heads, 128 pairs: 29.6 -> 28.1 us); runs
+// of twice the average would leave most SMs idle behind the longest.
+__device__ __forceinline__ Deal deal_out(const View& v, const int* pre, int grid, int c, bool may_be_whole,
+                                         DealShared* sh) {
+  Deal d;
+  d.pre = pre;
+  d.B = v.B;
+  d.Hk = v.Hk;
+  d.total = static_cast<long long>(pre[v.B]) * v.Hk;
+  const long long most = (d.total + kMinBlocks - 1) / kMinBlocks;
+  d.ctas = static_cast<int>(most < grid ? most : grid);
+  for (int i = threadIdx.x; i <= d.ctas && d.ctas > 0; i += blockDim.x) {
+    const long long x = share_of(d.total, i, d.ctas);
+    long long y = x;
+    int b = v.B, pb = v.B;
+    if (i < d.ctas) {
+      b = pb = d.sequence(x);
+      const int cnt = pre[b + 1] - pre[b], rem = static_cast<int>(x - static_cast<long long>(pre[b]) * v.Hk);
+      const int up = (rem + cnt - 1) / cnt * cnt;
+      y = x - rem + up;
+      if (up == cnt * v.Hk) {  // the next sequence's first pair
+        do ++pb;
+        while (pb < v.B && pre[pb + 1] == pre[pb]);
+      }
+    }
+    sh->begin[i] = x;
+    sh->pair[i] = y;
+    sh->b[i] = b;
+    sh->pair_b[i] = pb;
+  }
+  __syncthreads();
+  bool uneven = !may_be_whole;
+  for (int i = threadIdx.x; i < d.ctas; i += blockDim.x)
+    uneven = uneven || 4 * (sh->pair[i + 1] - sh->pair[i]) * d.ctas > 5 * d.total;
+  d.whole = !__syncthreads_or(uneven);
+  d.at = d.end = 0;
+  d.b = 0;
+  if (c < d.ctas) {
+    d.at = d.whole ? sh->pair[c] : sh->begin[c];
+    d.end = d.whole ? sh->pair[c + 1] : sh->begin[c + 1];
+    d.b = d.whole ? sh->pair_b[c] : sh->b[c];
+  }
+  return d;
+}
 
 template <int D, int MB>
 struct RowsSmem {
@@ -142,10 +175,8 @@ struct Walk {
   int B, Hk;
   long long at, end;
   int b, hk, t0, t1, cnt;
-  __device__ Walk(const Deal& deal, int c)
-      : pre(deal.pre), B(deal.B), Hk(deal.Hk), at(deal.begin(c)), end(deal.begin(c + 1)) {
-    if (at >= end) return;
-    b = deal.sequence(at);
+  __device__ explicit Walk(const Deal& deal)
+      : pre(deal.pre), B(deal.B), Hk(deal.Hk), at(deal.at), end(deal.end), b(deal.b) {
     set();
   }
   __device__ void set() {
@@ -220,11 +251,10 @@ __global__ void __launch_bounds__(32 * (kKeyGroups * MB + 1), 1)
   pdl_wait();
   const int c = blockIdx.x;
   fill_prefix(v, pre, 16 * MB, c == 0);
-  Deal deal(v, pre, gridDim.x);
-  __shared__ int s_longest;
-  deal.settle(&s_longest);
-  if (c >= deal.ctas) return;
-  Walk w(deal, c);
+  __shared__ DealShared s_deal;
+  const Deal deal = deal_out(v, pre, gridDim.x, c, true, &s_deal);
+  if (deal.at >= deal.end) return;
+  Walk w(deal);
   const WaitCtx wc{abort_flag, p.wait_ns};
 
   if (warp == kWarps) {

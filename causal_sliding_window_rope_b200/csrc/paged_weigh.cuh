@@ -77,9 +77,10 @@ __global__ void __launch_bounds__(32 * (4 * WeighGroups<NT>::value + 1), 1)
   }
   pdl_wait();
   fill_prefix(v, pre, p.max_rows, c == 0);
-  const Deal deal(v, pre, gridDim.x);
-  if (c >= deal.ctas) return;
-  Walk w(deal, c);
+  __shared__ DealShared s_deal;
+  const Deal deal = deal_out(v, pre, gridDim.x, c, false, &s_deal);
+  if (deal.at >= deal.end) return;
+  Walk w(deal);
   const WaitCtx wc{abort_flag, p.wait_ns};
 
   if (warp == kWarps) {
