@@ -12,6 +12,8 @@
 // checks a sequence before it touches it (seq_load) and reports one that does
 // not fit through the status word; such a sequence is left alone.
 #pragma once
+#include <climits>
+
 #include "prologue.cuh"
 #include "decode.cuh"
 
@@ -66,6 +68,36 @@ __device__ __forceinline__ int page_entry(const View& v, int row) {
 __device__ __forceinline__ int page_slot(const View& v, int row) {
   return v.page_shift >= 0 ? row & (v.page_size - 1) : row % v.page_size;
 }
+
+// Pages of a producer warp's units: lane l's unit is rows [row, row + unit) of
+// block 0, and the same of every `step` rows. The warp holds 32 entries of the
+// page table, one per lane, so the table's latency is paid once in 32 pages;
+// entries of rows that no token sees are not read, and the box of such a unit
+// lies past the pool, which reads as zeros.
+struct UnitPages {
+  const View& v;
+  const int* table;  // the sequence's row of the page table
+  int row, step, unit, lo, end, held, base;
+  static constexpr int kNone = INT_MIN;
+  __device__ UnitPages(const View& v_, int b, const Seq& s, int row_, int step_, int unit_)
+      : v(v_), table(v_.page_table + static_cast<size_t>(b) * v_.pages_per_seq), row(row_), step(step_), unit(unit_),
+        lo(max(0, s.L - v_.W + 1)), end(s.L + s.n), held(kNone), base(INT_MIN / 2) {}
+  // All lanes call; those with `mine` get their unit's page of block t.
+  __device__ int page(int t, bool mine) {
+    const int r = row + t * step, e = page_entry(v, r);
+    if (__any_sync(0xffffffffu, mine && (e < base || e >= base + 32))) {  // a block's units have at most 8 pages
+      base = __shfl_sync(0xffffffffu, e, 0);
+      const int mine_e = base + lane_id();
+      held = mine_e >= page_entry(v, lo) && mine_e <= page_entry(v, end - 1) ? table[mine_e] : kNone;
+    }
+    const int p = __shfl_sync(0xffffffffu, held, e - base);
+    if (!mine || r >= end || r + unit <= lo) return v.n_pages;
+    if (p >= 0 && p < v.n_pages) return p;
+    atomicOr(&g_status, kStatusRange);
+    return v.n_pages;
+  }
+  __device__ int slot(int t) const { return page_slot(v, row + t * step); }
+};
 
 // Row of a (pages, page_size, Hk) pool of K or V rows (in units of head_dim
 // elements) and of a (pages, Hk, page_size) pool of row terms.

@@ -106,13 +106,13 @@ struct DealShared {
   int b[kSMs + 1], pair_b[kSMs + 1];
 };
 
-// All threads call (at least as many as CTAs). With may_be_whole, whole pairs
+// All threads call. With sh (in shared memory), whole pairs
 // where no run then exceeds the average by a quarter: the SMs share HBM, so
 // the others' runs are read no slower, and nothing is left to join
 // (32 sequences of 2048 rows on 4 KV heads, 128 pairs: 29.6 -> 28.1 us); runs
 // of twice the average would leave most SMs idle behind the longest.
-__device__ __forceinline__ Deal deal_out(const View& v, const int* pre, int grid, int c, bool may_be_whole,
-                                         DealShared* sh) {
+// Without it (sh null) each thread works its CTA's run out for itself.
+__device__ __forceinline__ Deal deal_out(const View& v, const int* pre, int grid, int c, DealShared* sh) {
   Deal d;
   d.pre = pre;
   d.B = v.B;
@@ -120,6 +120,17 @@ __device__ __forceinline__ Deal deal_out(const View& v, const int* pre, int grid
   d.total = static_cast<long long>(pre[v.B]) * v.Hk;
   const long long most = (d.total + kMinBlocks - 1) / kMinBlocks;
   d.ctas = static_cast<int>(most < grid ? most : grid);
+  d.whole = false;
+  d.at = d.end = 0;
+  d.b = 0;
+  if (!sh) {
+    if (c < d.ctas) {
+      d.at = share_of(d.total, c, d.ctas);
+      d.end = share_of(d.total, c + 1, d.ctas);
+      d.b = d.sequence(d.at);
+    }
+    return d;
+  }
   for (int i = threadIdx.x; i <= d.ctas && d.ctas > 0; i += blockDim.x) {
     const long long x = share_of(d.total, i, d.ctas);
     long long y = x;
@@ -140,12 +151,10 @@ __device__ __forceinline__ Deal deal_out(const View& v, const int* pre, int grid
     sh->pair_b[i] = pb;
   }
   __syncthreads();
-  bool uneven = !may_be_whole;
+  bool uneven = false;
   for (int i = threadIdx.x; i < d.ctas; i += blockDim.x)
     uneven = uneven || 4 * (sh->pair[i + 1] - sh->pair[i]) * d.ctas > 5 * d.total;
   d.whole = !__syncthreads_or(uneven);
-  d.at = d.end = 0;
-  d.b = 0;
   if (c < d.ctas) {
     d.at = d.whole ? sh->pair[c] : sh->begin[c];
     d.end = d.whole ? sh->pair[c + 1] : sh->begin[c + 1];
@@ -252,7 +261,7 @@ __global__ void __launch_bounds__(32 * (kKeyGroups * MB + 1), 1)
   const int c = blockIdx.x;
   fill_prefix(v, pre, 16 * MB, c == 0);
   __shared__ DealShared s_deal;
-  const Deal deal = deal_out(v, pre, gridDim.x, c, true, &s_deal);
+  const Deal deal = deal_out(v, pre, gridDim.x, c, &s_deal);
   if (deal.at >= deal.end) return;
   Walk w(deal);
   const WaitCtx wc{abort_flag, p.wait_ns};
@@ -263,7 +272,7 @@ __global__ void __launch_bounds__(32 * (kKeyGroups * MB + 1), 1)
       prefetch_tmap(&tmK);
       prefetch_tmap(&tmV);
     }
-    const int nu = kBlk / p.unit, boxes = nu * NP;  // <= 8 boxes per operand
+    const int boxes = kBlk / p.unit * NP;  // <= 8 per operand; lane: unit and panel
     const int my_unit = lane / NP, my_panel = lane % NP;
     uint8_t* my_dst = smem + my_panel * SM::kPanel + my_unit * p.unit * 128;
     int stage = 0, use = 0, issued = 0;
@@ -273,33 +282,23 @@ __global__ void __launch_bounds__(32 * (kKeyGroups * MB + 1), 1)
       int first;
       seq_load(v, w.b, false, s);
       visible_blocks(v, s, 16 * MB, first);
-      const int lo = max(0, s.L - v.W + 1), end = s.L + s.n;
-      auto lookup = [&](int t) -> int {  // page of this lane's unit, or past the pool
-        const int r = (first + t) * kBlk + my_unit * p.unit;
-        if (lane >= boxes || r >= end || r + p.unit <= lo) return v.n_pages;
-        const int page = page_at(v, w.b, page_entry(v, r));
-        return page < 0 ? v.n_pages : page;
-      };
-      int page = lookup(w.t0);
+      UnitPages up(v, w.b, s, first * kBlk + my_unit * p.unit, kBlk, p.unit);
       for (int t = w.t0; t < w.t1; ++t) {
-        const int next = t + 1 < w.t1 ? lookup(t + 1) : 0;
-        if (use > 0) {
-          ok = __all_sync(0xffffffffu, mbar_wait(&empty[stage], (use - 1) & 1, wc));
-          if (!ok) break;
-        }
+        const int page = up.page(t, lane < boxes);
+        if (use > 0) ok = __all_sync(0xffffffffu, mbar_wait(&empty[stage], (use - 1) & 1, wc));
+        if (!ok) break;
         if (lane == 0) {
           mbar_expect_tx(&full_k[stage], SM::kOp);
           mbar_expect_tx(&full_v[stage], SM::kOp);
         }
         __syncwarp();
         if (lane < boxes) {
-          const int slot = page_slot(v, (first + t) * kBlk + my_unit * p.unit);
+          const int slot = up.slot(t);
           uint8_t* dst = my_dst + stage * SM::kStage;
           tma_load_4d(&tmK, &full_k[stage], dst, 64 * my_panel, w.hk, slot, page);
           tma_load_4d(&tmV, &full_v[stage], dst + SM::kOp, 64 * my_panel, w.hk, slot, page);
         }
         ++issued;
-        page = next;
         if (++stage == NS) {
           stage = 0;
           ++use;

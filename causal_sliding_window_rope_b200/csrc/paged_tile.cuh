@@ -142,18 +142,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       int slot = 0, use = 0, issued = 0, segs = 0, q_issued = 0;
       bool ok = true;
       for (TileWalk w(p, run); ok && w.valid(); w.next(), ++segs) {
-        const int b = w.seq();
-        const int lo = max(0, w.s.L - v.W + 1), end = w.s.L + w.s.n;
-        auto lookup = [&](int t) -> int {  // page of this lane's unit, or past the pool
-          const int r = (w.first + t) * 128 + my_unit * p.unit;
-          if (lane >= boxes || r >= end || r + p.unit <= lo) return v.n_pages;
-          const int page = page_at(v, b, page_entry(v, r));
-          return page < 0 ? v.n_pages : page;
-        };
-        int page = lookup(w.t0);
+        UnitPages up(v, w.seq(), w.s, w.first * 128 + my_unit * p.unit, 128, p.unit);
         for (int t = w.t0; ok && t < w.t1; ++t) {
-          const int next = t + 1 < w.t1 ? lookup(t + 1) : 0;
-          const int row_slot = page_slot(v, (w.first + t) * 128 + my_unit * p.unit);
+          const int page = up.page(t, lane < boxes), row_slot = up.slot(t);
 #pragma unroll
           for (int kind = 0; kind < 2; ++kind) {
             if (use > 0) ok = ok && __all_sync(0xffffffffu, mbar_wait(&kv_empty[slot], (use - 1) & 1, wc));
@@ -185,7 +176,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             ++q_issued;
             __syncwarp();
           }
-          page = next;
         }
         if (!ok) break;
       }

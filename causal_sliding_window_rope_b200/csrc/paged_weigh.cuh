@@ -77,8 +77,7 @@ __global__ void __launch_bounds__(32 * (4 * WeighGroups<NT>::value + 1), 1)
   }
   pdl_wait();
   fill_prefix(v, pre, p.max_rows, c == 0);
-  __shared__ DealShared s_deal;
-  const Deal deal = deal_out(v, pre, gridDim.x, c, false, &s_deal);
+  const Deal deal = deal_out(v, pre, gridDim.x, c, nullptr);
   if (deal.at >= deal.end) return;
   Walk w(deal);
   const WaitCtx wc{abort_flag, p.wait_ns};
@@ -86,7 +85,7 @@ __global__ void __launch_bounds__(32 * (4 * WeighGroups<NT>::value + 1), 1)
   if (warp == kWarps) {
     // ---------------------------------------------------- producer
     if (lane == 0) prefetch_tmap(&tmK);
-    const int boxes = (kBlk / p.unit) * NP;
+    const int boxes = kBlk / p.unit * NP;  // as in rows_kernel
     const int my_unit = lane / NP, my_panel = lane % NP;
     uint8_t* my_dst = smem + my_panel * SM::kPanel + my_unit * p.unit * 128;
     int stage = 0, use = 0, issued = 0;
@@ -96,27 +95,16 @@ __global__ void __launch_bounds__(32 * (4 * WeighGroups<NT>::value + 1), 1)
       int first;
       seq_load(v, w.b, false, s);
       visible_blocks(v, s, p.max_rows, first);
-      const int lo = max(0, s.L - v.W + 1), end = s.L + s.n;
-      auto lookup = [&](int t) -> int {
-        const int r = (first + t) * kBlk + my_unit * p.unit;
-        if (lane >= boxes || r >= end || r + p.unit <= lo) return v.n_pages;
-        const int page = page_at(v, w.b, page_entry(v, r));
-        return page < 0 ? v.n_pages : page;
-      };
-      int page = lookup(w.t0);
+      UnitPages up(v, w.b, s, first * kBlk + my_unit * p.unit, kBlk, p.unit);
       for (int t = w.t0; t < w.t1; ++t) {
-        const int next = t + 1 < w.t1 ? lookup(t + 1) : 0;
-        if (use > 0) {
-          ok = __all_sync(0xffffffffu, mbar_wait(&empty[stage], (use - 1) & 1, wc));
-          if (!ok) break;
-        }
+        const int page = up.page(t, lane < boxes);
+        if (use > 0) ok = __all_sync(0xffffffffu, mbar_wait(&empty[stage], (use - 1) & 1, wc));
+        if (!ok) break;
         if (lane == 0) mbar_expect_tx(&full[stage], SM::kStage);
         __syncwarp();
         if (lane < boxes)
-          tma_load_4d(&tmK, &full[stage], my_dst + stage * SM::kStage, 64 * my_panel, w.hk,
-                      page_slot(v, (first + t) * kBlk + my_unit * p.unit), page);
+          tma_load_4d(&tmK, &full[stage], my_dst + stage * SM::kStage, 64 * my_panel, w.hk, up.slot(t), page);
         ++issued;
-        page = next;
         if (++stage == NS) {
           stage = 0;
           ++use;
@@ -327,20 +315,15 @@ __global__ void __launch_bounds__(kWeighThreads, 2)
     }
     int nk = 0, nq = 0;
     for (; ok && w.valid(); w.next()) {
-      const int lo = max(0, w.s.L - v.W + 1), end = w.s.L + w.s.n;
-      const int r = w.units.first_row(v, w.s, w.u) + my_unit * p.unit;
-      int page = v.n_pages;  // past the pool: zeros
-      if (lane < boxes && r < end && r + p.unit > lo) {
-        page = page_at(v, w.seq(), page_entry(v, r));
-        if (page < 0) page = v.n_pages;
-      }
+      UnitPages up(v, w.seq(), w.s, w.units.first_row(v, w.s, w.u) + my_unit * p.unit, 128, p.unit);
+      const int page = up.page(0, lane < boxes);
       if (nk > 0) ok = __all_sync(0xffffffffu, mbar_wait(k_empty, (nk - 1) & 1, wc));
       if (!ok) break;
       if (lane == 0) mbar_expect_tx(k_full, SM::kOp);
       __syncwarp();
       if (lane < boxes)
         tma_load_4d(&tmK, k_full, smem + my_panel * SM::kPanel + my_unit * p.unit * 128, 64 * my_panel, w.hk,
-                    page_slot(v, r), page);
+                    up.slot(0), page);
       ++nk;
       // Terms of the query rows lane, lane + 32, ... of a tile: loaded one tile
       // ahead, written behind the wait for the tile's slot, which needs no
