@@ -123,6 +123,12 @@ __global__ void __launch_bounds__(32 * (4 * WeighGroups<NT>::value + 1), 1)
   const int a_row = key_w + (lane & 7) + ((lane >> 3) & 1) * 8;
   int at = 0;  // blocks of the CTA so far
   for (; w.valid(); w.next()) {
+    // Pairs of fewer blocks than there are groups: only the groups that have
+    // one load the query rows, the others go on to the next pair.
+    if ((group - at % kGroups + kGroups) % kGroups >= w.t1 - w.t0) {
+      at += w.t1 - w.t0;
+      continue;
+    }
     Seq s;
     int first;
     seq_load(v, w.b, false, s);
