@@ -486,11 +486,12 @@ cswattn_status attn_paged_select(const cswattn_layer* layer, const cswattn_paged
   sp.src = src;
   sp.dst = dst;
   sp.new_len = new_len;
-  if ((st = set_smem(paged::select_kernel, paged::kSelectMaxKeys * 4)) != CSWATTN_OK) return st;
+  const auto kernel = ranks > 1 ? paged::select_kernel<true> : paged::select_kernel<false>;
+  if ((st = set_smem(kernel, paged::kSelectMaxKeys * 4)) != CSWATTN_OK) return st;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   {
     ScopedTiming tm(CSWATTN_K_DECODE, cs);
-    launch_pdl_cluster(paged::select_kernel, dim3(ranks, s.Hk, s.B), dim3(paged::kSelectThreads),
+    launch_pdl_cluster(kernel, dim3(ranks, s.Hk, s.B), dim3(paged::kSelectThreads),
                        static_cast<size_t>(sp.smem_keys) * 4, static_cast<unsigned>(ranks), cs, sp);
   }
   return launched("paged select launch");

@@ -65,7 +65,16 @@ __device__ __forceinline__ uint2 peer_load2(const void* p, int rank) {
 // shared memory), long heads are spread over up to 8 SMs, and what the
 // others have to know of a CTA's rows is exchanged once. Every path of a
 // cluster's CTAs meets the same barriers.
+// A lone CTA (CLUSTER false) meets itself at the block's barrier and reads its own counts.
+template <bool CLUSTER>
 __global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectParams p) {
+  const int ranks = CLUSTER ? gridDim.x : 1;
+  auto meet = [] {
+    if constexpr (CLUSTER) cluster_sync();
+    else __syncthreads();
+  };
+  auto load1 = [](const uint32_t* x, int k) { return CLUSTER ? peer_load(x, k) : *x; };
+  auto load2 = [](const void* x, int k) { return CLUSTER ? peer_load2(x, k) : *static_cast<const uint2*>(x); };
   extern __shared__ uint32_t s_key[];
   __shared__ uint32_t s_hist[2][kBins];          // two, so that a pass needs one meeting of the cluster
   __shared__ __align__(8) uint32_t s_sum[2][64];  // of 32 bins each
@@ -74,7 +83,7 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectPara
   __shared__ __align__(8) uint2 s_count[2];      // the same of this CTA
   __shared__ uint32_t s_before[3], s_total;      // ties, holes, movers of the CTAs before it; movers of all
   const View& v = p.v;
-  const int rank = blockIdx.x, ranks = gridDim.x, hk = blockIdx.y, b = blockIdx.z;
+  const int rank = CLUSTER ? blockIdx.x : 0, hk = blockIdx.y, b = blockIdx.z;
   const int warp = warp_id(), lane = lane_id(), tid = threadIdx.x;
   pdl_launch_dependents();
   for (int i = tid; i < 2 * kBins; i += kSelectThreads) (&s_hist[0][0])[i] = 0u;
@@ -169,14 +178,14 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectPara
       const uint32_t x = __reduce_add_sync(0xffffffffu, hist[(2 * warp + j) * 32 + lane]);
       if (lane == 0) s_sum[d & 1][2 * warp + j] = x;
     }
-    cluster_sync();
+    meet();
     if (warp == 0) {
       uint2 x = make_uint2(0u, 0u);  // sums 2 lane and 2 lane + 1 of all CTAs
       uint32_t y = 0u;               // then a bin
 #pragma unroll
       for (int j = 0; j < kSelectMaxCluster; ++j) {
         if (j >= ranks) break;
-        const uint2 t = peer_load2(&s_sum[d & 1][2 * lane], (rank + j) % ranks);
+        const uint2 t = load2(&s_sum[d & 1][2 * lane], (rank + j) % ranks);
         x.x += t.x;
         x.y += t.y;
       }
@@ -190,7 +199,7 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectPara
 #pragma unroll
       for (int j = 0; j < kSelectMaxCluster; ++j) {
         if (j >= ranks) break;
-        y += peer_load(&hist[at * 32 + lane], (rank + j) % ranks);
+        y += load1(&hist[at * 32 + lane], (rank + j) % ranks);
       }
       pick(y, rest, bin, rest);
       if (lane == 0) {
@@ -257,13 +266,13 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectPara
       s_count[1] = make_uint2(t[2], t[3]);
     }
   }
-  cluster_sync();
+  meet();
   if (warp == 0) {  // lane k: CTA k
     uint2 ties = make_uint2(0u, 0u), more = make_uint2(0u, 0u);
     uint32_t holes = 0u, movers = 0u;
     if (lane < ranks) {
-      ties = peer_load2(&s_count[0], lane);
-      more = peer_load2(&s_count[1], lane);
+      ties = load2(&s_count[0], lane);
+      more = load2(&s_count[1], lane);
     }
     const uint32_t ties_before = before_lane(ties.x + ties.y);
     const int first = min(L, lane * per), last = min(L, first + per);
@@ -308,7 +317,7 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectPara
   const int total = static_cast<int>(s_total);
   if (lead && tid == 0) p.n_moves[head] = total;
   for (int i = total + rank * kSelectThreads + tid; i < p.n_keep; i += ranks * kSelectThreads) src[i] = dst[i] = -1;
-  cluster_sync();  // no CTA leaves while another may still read its counts
+  if constexpr (CLUSTER) cluster_sync();  // no CTA leaves while another may still read its counts
 }
 
 struct MoveParams {
