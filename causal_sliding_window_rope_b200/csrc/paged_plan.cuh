@@ -33,10 +33,11 @@ struct Plan {
   Start start[kMaxRuns];
 };
 
-// A CTA's run: `left` blocks from st on; none when left is 0.
+// A CTA's run: `left` blocks from st on (in sequence s); none when left is 0.
 struct Run {
   Start st;
   long long left;
+  Seq s;
 };
 
 // Sequences with more query rows (new tokens x heads of a group) than short_rows.
@@ -181,6 +182,7 @@ __device__ __forceinline__ void find_run(const View& v, const Units& units, int 
           const Start st{lo, static_cast<int>(rem / cnt), u, static_cast<int>(left) - (inc - mine)};
           plan->start[c] = st;
           run->st = st;
+          run->s = s;
           run->left = share_of(total, c + 1, ctas) - at;
         }
         if (__any_sync(0xffffffffu, here)) break;
@@ -201,8 +203,9 @@ struct UnitWalk {
   int k, hk, u, t0, t1, cnt, n_units, first;
   Seq s;
   __device__ UnitWalk(const View& v_, const Units& units_, const Run& run, const int* longs_)
-      : v(v_), units(units_), longs(longs_), left(run.left), k(run.st.k), hk(run.st.hk), u(run.st.unit), t0(run.st.t0) {
-    load();
+      : v(v_), units(units_), longs(longs_), left(run.left), k(run.st.k), hk(run.st.hk), u(run.st.unit), t0(run.st.t0),
+        s(run.s) {
+    n_units = units.count(v, s);
     set();
   }
   __device__ int seq() const { return longs[k]; }
