@@ -14,6 +14,7 @@
 
 #include <climits>
 #include <cstdarg>
+#include <string>
 
 #include "../../include/cswattn.h"
 
@@ -39,7 +40,7 @@ struct {
 // Thrown behind a set Python exception; nothing passes the module's functions.
 struct Raised {};
 
-[[noreturn]] void raise(PyObject* type, const char* fmt, ...) {
+[[noreturn]] __attribute__((format(printf, 2, 3))) void raise(PyObject* type, const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);
   PyErr_FormatV(type, fmt, ap);
@@ -104,6 +105,12 @@ constexpr auto kBf16 = at::kBFloat16;
 constexpr auto kF32 = at::kFloat;
 constexpr auto kI32 = at::kInt;
 
+std::string dims(at::IntArrayRef a) {
+  std::string s = "(";
+  for (size_t i = 0; i < a.size(); ++i) s += (i ? ", " : "") + std::to_string(a[i]);
+  return s + ")";
+}
+
 // The address of a contiguous CUDA tensor of this type and shape on the
 // device (which the first tensor of a call sets when it is -1).
 void* want(const char* name, PyObject* o, at::ScalarType type, at::IntArrayRef shape, int& device) {
@@ -115,10 +122,11 @@ void* want(const char* name, PyObject* o, at::ScalarType type, at::IntArrayRef s
   if (device < 0) device = on;
   if (on != device)
     raise(PyExc_ValueError, "%s lies on cuda:%d, other tensors of the call on cuda:%d", name, on, device);
-  if (t.scalar_type() != type)
+  if (t.scalar_type() != type) {
     raise(PyExc_ValueError, "%s must be %s, got %s", name, c10::toString(type), c10::toString(t.scalar_type()));
+  }
   if (t.sizes() != shape) {
-    const std::string want_ = c10::str(shape), got = c10::str(t.sizes());
+    const std::string want_ = dims(shape), got = dims(t.sizes());
     raise(PyExc_ValueError, "%s must have shape %s, got %s", name, want_.c_str(), got.c_str());
   }
   if (!t.is_contiguous()) raise(PyExc_ValueError, "%s must be contiguous", name);

@@ -224,6 +224,106 @@ def test_pages_before_the_window_are_not_read():
     assert abs(w.double().sum().item() - c.H * sum(c.news)) <= 1e-4 * c.H * sum(c.news)
 
 
+def test_many_sequences():
+    """More sequences than threads of a CTA, most of them without a row or a token."""
+    r = np.random.RandomState(4)
+    B = 1500
+    news = [int(x) for x in r.choice([0, 0, 0, 1, 1, 2, 40], B)]
+    lens = [int(x) for x in r.choice([0, 1, 15, 16, 30], B)]
+    c = Case(lens, news, 4, 2, 64, 16, seed=41, pad=2).fill()
+    q = c.queries()
+    O, lse = run_attend(c, q)
+    cs.cswattn_sync_status()
+    wO, wl, tO, tl = ref.attention(c, q)
+    within(O, wO, tO, "O")
+    within(lse, wl, tl, "lse")
+    w0 = c.randn(c.n_pages, 2, 16).abs()
+    cache = cs.PagedCache(c.spec, k=c.k_pages.cuda(), weight=w0.cuda())
+    cs.attn_paged_weigh(c.spec, c.batch(), cache, q.cuda(), wl.float().cuda())
+    cs.cswattn_sync_status()
+    want, tol = ref.weights(c, q, wl.float(), w0)
+    within(cache.weight, want, tol, "weight")
+
+
+def test_the_largest_number_of_sequences():
+    """4096 sequences of one row and one token: each attends to its two rows."""
+    B, H, Hk, D = 4096, 2, 1, 64
+    c = Case([1] * B, [1] * B, H, Hk, D, 16, seed=42, spare=0)
+    k, v = torch.randn(B, 16, Hk, D, generator=c.g).to(BF), torch.randn(B, 16, Hk, D, generator=c.g).to(BF)
+    k[:, 2:], v[:, 2:] = NAN, NAN
+    c.k_pages[c.table[:, 0].long()], c.v_pages[c.table[:, 0].long()] = k, v
+    q = c.queries()
+    O, lse = run_attend(c, q)
+    cs.cswattn_sync_status()
+    s = torch.einsum("bhd,bjd->bhj", q.double(), k[:, :2, 0].double()) * D ** -0.5
+    want = torch.softmax(s, -1) @ v[:, :2, 0].double()
+    mag = torch.softmax(s, -1) @ v[:, :2, 0].double().abs()
+    within(O, want, 2.0 ** -8 * (mag + want.abs()) + 1e-3 * mag, "O")
+    within(lse, torch.logsumexp(s, -1), torch.full((B, H), 1e-4, dtype=torch.float64), "lse")
+
+
+def test_a_stream_by_handle_and_a_workspace_of_the_callers():
+    c = Case([300, 20], [70, 1], 4, 2, 128, 32, seed=43).fill()
+    q = c.queries().cuda()
+    lse = ref.attention(c, q.cpu())[1].float().cuda()
+    batch, got = c.batch(), []
+    side = torch.cuda.Stream()
+    for kind in ("own", "default", "handle", "stream"):
+        cache = cs.PagedCache(c.spec, k=c.k_pages.cuda(), weight=torch.zeros(c.n_pages, 2, 32, device="cuda"))
+        torch.cuda.synchronize()
+        if kind == "own":
+            ws = torch.empty(cs.attn_paged_weigh_workspace_bytes(c.spec, batch, cache), dtype=torch.uint8, device="cuda")
+            cs.attn_paged_weigh(c.spec, batch, cache, q, lse, workspace=ws)
+        elif kind == "default":
+            cs.attn_paged_weigh(c.spec, batch, cache, q, lse)
+        else:
+            cs.attn_paged_weigh(c.spec, batch, cache, q, lse, stream=side.cuda_stream if kind == "handle" else side)
+        torch.cuda.synchronize()
+        got.append(cache.weight)
+    assert got[0].sum() > 0 and all(torch.equal(got[0], w) for w in got[1:])
+
+
+def test_tensors_that_do_not_fit_are_refused():
+    """Types, shapes, strides, hosts and missing pools: before anything is enqueued."""
+    c = Case([30, 20], [3, 1], 4, 2, 128, 16, seed=44).fill()
+    q, batch = c.queries().cuda(), c.batch()
+    cache = cs.PagedCache(c.spec, k=c.k_pages.cuda(), v=c.v_pages.cuda())
+    O, lse = torch.zeros_like(q), torch.zeros(c.N, 4, device="cuda")
+    ws = torch.empty(cs.attn_paged_workspace_bytes(c.spec, batch, cache), dtype=torch.uint8, device="cuda")
+    wide = torch.zeros(c.N, 4, 256, dtype=BF, device="cuda")[..., ::2]
+    for change in (dict(q_out=q.float()), dict(q_out=q[:2]), dict(q_out=wide), dict(q_out=q.cpu()), dict(O=None),
+                   dict(lse=lse.double()), dict(lse=lse[:, :3]), dict(workspace=ws.cpu()), dict(workspace=ws[::2])):
+        args = {**dict(q_out=q, O=O, lse=lse, workspace=ws), **change}
+        with pytest.raises(ValueError):
+            cs.attn_paged(c.spec, batch, cache, **args)
+    with pytest.raises(TypeError):
+        cs.attn_paged(c.spec, batch, cache, q.tolist(), O, lse, ws)
+    with pytest.raises(cs.CswattnError) as err:  # less than the call needs, said by the caller or by the tensor
+        cs.attn_paged(c.spec, batch, cache, q, O, lse, ws, workspace_bytes=ws.numel() - 1)
+    assert err.value.status == cs.ERR_INVALID_ARG
+    with pytest.raises(cs.CswattnError):
+        cs.attn_paged(c.spec, batch, cache, q, O, lse, ws[:256], workspace_bytes=1 << 40)
+    with pytest.raises(ValueError, match="weight"):  # no pool to add to
+        cs.attn_paged_weigh(c.spec, batch, cache, q, lse)
+    other = cs.LayerSpec(2, c.cap, 4, 4, 128, c.cap, has_ve=False)
+    with pytest.raises(ValueError):  # a cache of another layer
+        cs.attn_paged(other, batch, cache, q, O, lse, ws)
+    with pytest.raises(ValueError, match="sequences"):
+        cs.attn_paged(cs.LayerSpec(3, c.cap, 4, 2, 128, c.cap, has_ve=False), batch, cache, q, O, lse, ws)
+    i64 = lambda t: t.to(torch.int64)  # noqa: E731
+    for a in ((i64(batch.page_table), batch.cache_len, batch.new_start), (batch.page_table, i64(batch.cache_len), None),
+              (batch.page_table, batch.cache_len[:1], None), (batch.page_table, batch.cache_len, batch.cache_len),
+              (batch.page_table.cpu(), batch.cache_len, None), (batch.page_table.T, batch.cache_len, None)):
+        with pytest.raises(ValueError):
+            cs.PagedBatch(*a)
+    with pytest.raises(ValueError):
+        cs.PagedCache(c.spec, k=c.k_pages.cuda(), v=c.v_pages[:-1].cuda())
+    with pytest.raises(ValueError):
+        cs.attn_paged_append(c.spec, cs.PagedBatch(batch.page_table, batch.cache_len, None, c.N, 3), cache, q, q, q, None, None, O)
+    assert (O == 0).all() and (lse == 0).all()
+    cs.cswattn_sync_status()
+
+
 # ------------------------------------------------------------------ select and move
 
 SELECT = [
@@ -237,7 +337,7 @@ SELECT = [
     ([700], 2, 64, 16, 3, 2, None, True),
     ([5000, 4999], 2, 128, 256, 1300, 500, 6000, True),
     ([33000], 1, 64, 128, 20000, 5, None, True),
-    ([60001], 1, 64, 128, 700, 20, None, True),     # past the rows held in shared memory
+    ([60001], 1, 64, 128, 700, 20, None, True),
 ]
 
 
@@ -284,6 +384,28 @@ def test_select(lens, Hk, D, page, n_keep, n_recent, cap, ties):
     got = run_select(c, w, pos, next_pos, n_keep, n_recent)
     cs.cswattn_sync_status()
     check_select(c, w, pos, next_pos, n_keep, n_recent, got)
+
+
+def test_select_beyond_shared_memory():
+    """A head of more rows than its CTA holds in shared memory (so many heads that none has a second CTA): the rows
+    past them are read again in every pass."""
+    B, L, K = 75, 60000, 20000
+    c = Case([L] + [3] * (B - 1), [0] * B, 1, 1, 64, 128, cap=L, seed=50)
+    w = torch.round(torch.exp(2 * c.randn(c.n_pages, 1, 128)))
+    pos = torch.randint(0, 2 * L, (c.n_pages, 1, 128), generator=c.g, dtype=torch.int32)
+    next_pos = torch.tensor([2 * L] + [6] * (B - 1))
+    n, src, dst, new_len = (t.cpu() for t in run_select(c, w, pos, next_pos, K, 900))
+    cs.cswattn_sync_status()
+    wt, ps = head_rows(c, 0, 0, w).double().numpy(), head_rows(c, 0, 0, pos).numpy()
+    key = np.where(ps >= 2 * L - 900, np.inf, wt)
+    kept = np.zeros(L, bool)
+    kept[np.argsort(-key, kind="stable")[:K]] = True
+    rows = np.arange(L)
+    s, d = rows[kept & (rows >= K)], rows[~kept & (rows < K)]
+    m = int(n[0, 0])
+    assert m == len(s) == len(d) and int(new_len[0]) == K
+    assert (src[0, 0, :m].numpy() == s).all() and (dst[0, 0, :m].numpy() == d).all() and (src[0, 0, m:] == -1).all()
+    assert (n[1:] == 0).all() and (new_len[1:] == 3).all() and (src[1:] == -1).all() and (dst[1:] == -1).all()
 
 
 @pytest.mark.parametrize("kind", ["equal", "nan", "infinite", "signed", "all recent", "denormal"])
