@@ -444,25 +444,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool acc_ok = ok && mbar_wait(acc_full, 0, wc);
     if (__all_sync(0xffffffffu, acc_ok)) {
       tc_fence_after();
-      const float keep = N > 0 ? 1.f : 0.f;  // a part without steps writes zeros
+      // A part without steps writes zeros: its accumulators hold what the
+      // last kernel left in TMEM, which times zero may still be a NaN.
+      const bool any = N > 0;
       uint8_t* stv = smem + kOffQD;           // dV panels
       uint8_t* stk = stv + 4 * kF32Panel;     // dK panels
       auto stage_row = [&](uint8_t* panel, const uint32_t (&a)[32], float sc) {
 #pragma unroll
         for (int k = 0; k < 8; ++k)
           *reinterpret_cast<float4*>(panel + r * 128 + ((k ^ (r & 7)) << 4)) =
-              make_float4(__uint_as_float(a[4 * k]) * sc, __uint_as_float(a[4 * k + 1]) * sc,
-                          __uint_as_float(a[4 * k + 2]) * sc, __uint_as_float(a[4 * k + 3]) * sc);
+              any ? make_float4(__uint_as_float(a[4 * k]) * sc, __uint_as_float(a[4 * k + 1]) * sc,
+                                __uint_as_float(a[4 * k + 2]) * sc, __uint_as_float(a[4 * k + 3]) * sc)
+                  : make_float4(0.f, 0.f, 0.f, 0.f);
       };
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
         uint32_t a[32];
         tmem_ld32(tmem + lane_off + kColDV + c * 32, a);
         tmem_ld_wait();
-        stage_row(stv + c * kF32Panel, a, keep);
+        stage_row(stv + c * kF32Panel, a, 1.f);
         tmem_ld32(tmem + lane_off + kColDK + c * 32, a);
         tmem_ld_wait();
-        stage_row(stk + c * kF32Panel, a, p.scale * keep);
+        stage_row(stk + c * kF32Panel, a, p.scale);
       }
       fence_proxy_async_smem();
       mbar_arrive(kv_staged);

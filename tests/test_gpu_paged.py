@@ -657,6 +657,30 @@ def test_serving_loop_with_eviction(rope):
         assert torch.isfinite(s.cache.weight).all() and (s.cache.weight >= 0).all()
 
 
+@pytest.mark.parametrize("B,T,H,Hk,W", [(1, 128, 2, 2, 128), (2, 300, 4, 2, 300)])
+def test_dense_backward_after_scores_of_nan(B, T, H, Hk, W):
+    """What a kernel leaves in tensor memory is nobody's input: the dense layer's gradients are as before after an
+    attention over NaN rows (a backward part that has no step once multiplied what it found there by zero)."""
+    from _helpers import make_inputs
+    spec = cs.LayerSpec(B, T, H, Hk, 128, W, has_ve=True)
+    dev = {n: t.cuda() for n, t in make_inputs(B, T, H, Hk, 128, True, "bf16", config=98).items()}
+    c = Case([2000], [1500], 16, 4, 128, 128, seed=61)  # its pages are NaN; work for every SM
+    q, outs = c.queries(), []
+    for dirty in (False, True):
+        if dirty:
+            O, _ = run_attend(c, q)
+            cs.cswattn_sync_status()
+            assert torch.isnan(O.float()).all()
+        buf = cs.LayerBuffers(spec)
+        cs.layer_forward(spec, buf, dev["q"], dev["k"], dev["v"], dev["ve"], dev["gate"])
+        cs.layer_backward(spec, buf, dev["q"], dev["k"], dev["ve"], dev["gate"], dev["dO"])
+        cs.cswattn_sync_status()
+        outs.append([t.float() for t in (buf.O, buf.lse, buf.dQ, buf.dK, buf.dV, buf.dve, buf.dgate)])
+    for clean, after in zip(*outs):
+        assert torch.isfinite(after).all()
+        assert (clean - after).abs().max() <= 1e-2 * clean.abs().max()  # dQ adds its parts in any order
+
+
 def test_a_captured_loop_replays():
     """Append, attend, weigh, select and move in one CUDA graph, replayed on new inputs; two graphs share a workspace."""
     c = Case([40, 90], [1, 1], 4, 2, 64, 16, cap=120, ve=False, seed=31).fill()
