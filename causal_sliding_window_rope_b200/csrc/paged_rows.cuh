@@ -28,7 +28,7 @@ namespace paged {
 
 constexpr int kBlk = 64;         // cached rows of a block
 constexpr int kKeyGroups = 4;    // warps that share a block, 16 rows each
-constexpr int kMinBlocks = 2;    // fewest blocks worth a CTA of their own
+constexpr int kMinBlocks = 2;    // fewest blocks worth a CTA of their own (one chat over 1000 rows: 1 10.8 us, 2 9.8, 4 10.6)
 
 struct RowsParams {
   View v;
