@@ -72,46 +72,46 @@ int page_unit(int page_size, int most) {
   return u;
 }
 
+// A call whose sequences have at most 32 query rows (new tokens x heads of a
+// group) each runs rows_kernel; any other runs tile_kernel for all of its
+// sequences: few rows leave most of a tile empty there, but it reads the
+// cache as fast, and one launch of each kind fewer counts (31 single tokens
+// over 2000 rows beside a chunk of 512 tokens 61 us, 71 with rows_kernel for
+// the 31; 200 over 300 rows beside a chunk of 64 63 us, 74).
 struct PagedWorkspace {
+  bool tiles;
+  int rows;  // query rows of a share: 16 or 32, or a unit's 256
   float* part_o;
   float2* part_ml;
-  int2* info;
-  int slot_rows;  // query rows of a slot: 16, or 32 where a sequence may have more
-  bool tiles;     // a sequence may have more query rows than that
-  paged::Plan* plan;
+  int2* info;          // rows_kernel: the pairs' shares
+  paged::Plan* plan;   // tile_kernel: the CTAs' runs, and the sequences in order
   int* longs;
-  float* tile_o;
-  float2* tile_ml;
   size_t bytes;
 };
 
 PagedWorkspace carve_paged(const Shape& s, const paged::View& v, void* base) {
   uint8_t* p = static_cast<uint8_t*>(base);
   PagedWorkspace w;
-  w.slot_rows = static_cast<long long>(v.max_new) * s.g <= 16 ? 16 : 32;
-  const size_t rows = static_cast<size_t>(2 * paged::kSMs) * w.slot_rows;
+  const long long most = static_cast<long long>(v.max_new) * s.g;
+  w.tiles = most > 32;
+  w.rows = w.tiles ? 256 : (most > 16 ? 32 : 16);
+  const size_t rows = static_cast<size_t>(2 * paged::kSMs) * w.rows;
   size_t off = 0;
-  w.part_o = reinterpret_cast<float*>(p + off);
-  off += pad256(rows * s.D * 4);
-  w.part_ml = reinterpret_cast<float2*>(p + off);
-  off += pad256(rows * 8);
-  w.info = reinterpret_cast<int2*>(p + off);
-  off += pad256(static_cast<size_t>(s.B) * s.Hk * 8);
-  w.tiles = static_cast<long long>(v.max_new) * s.g > w.slot_rows;
+  auto take = [&](size_t bytes) {
+    void* at = p + off;
+    off += pad256(bytes);
+    return at;
+  };
+  w.part_o = static_cast<float*>(take(rows * s.D * 4));
+  w.part_ml = static_cast<float2*>(take(rows * 8));
+  w.info = nullptr;
   w.plan = nullptr;
   w.longs = nullptr;
-  w.tile_o = nullptr;
-  w.tile_ml = nullptr;
   if (w.tiles) {
-    const size_t tile_rows = static_cast<size_t>(2 * paged::kSMs) * 256;
-    w.plan = reinterpret_cast<paged::Plan*>(p + off);
-    off += pad256(sizeof(paged::Plan));
-    w.longs = reinterpret_cast<int*>(p + off);
-    off += pad256(static_cast<size_t>(s.B) * 4);
-    w.tile_o = reinterpret_cast<float*>(p + off);
-    off += pad256(tile_rows * s.D * 4);
-    w.tile_ml = reinterpret_cast<float2*>(p + off);
-    off += pad256(tile_rows * 8);
+    w.plan = static_cast<paged::Plan*>(take(sizeof(paged::Plan)));
+    w.longs = static_cast<int*>(take(static_cast<size_t>(s.B) * 4));
+  } else {
+    w.info = static_cast<int2*>(take(static_cast<size_t>(s.B) * s.Hk * 8));
   }
   w.bytes = off;
   return w;
@@ -145,27 +145,28 @@ void launch_rows_kernel(const paged::RowsParams& rp, const CUtensorMap& mk, cons
              static_cast<size_t>(paged::RowsSmem<D, MB>::kBytes) + 4 * (rp.v.B + 1), st, mk, mv, rp);
 }
 
-// The attention of few query rows, that of many, and the join of what both have cut. With prepare_only, sets
-// what the launches need: a call that may fail is made before anything of an
-// entry point is enqueued.
+// The attention of few query rows or that of many, and the join of what it
+// has cut. With prepare_only, sets what the launches need: a call that may
+// fail is made before anything of an entry point is enqueued.
 template <int D>
 cswattn_status launch_paged(const paged::RowsParams& rp, const paged::TileParams& tp, const paged::JoinParams& jp,
                             bool tiles, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mq,
-                            const CUtensorMap& mk128, const CUtensorMap& mv128, cudaStream_t st, bool prepare_only) {
-  const bool wide = jp.max_rows > 16;
+                            cudaStream_t st, bool prepare_only) {
+  const bool wide = jp.rows > 16;
   if (prepare_only) {
-    cswattn_status e = wide ? prepare_rows_kernel<D, 2>() : prepare_rows_kernel<D, 1>();
-    if (e != CSWATTN_OK || !tiles) return e;
-    return set_smem(paged::tile_kernel<D>, paged::TileSmem<D>::kBytes);
+    if (tiles) return set_smem(paged::tile_kernel<D>, paged::TileSmem<D>::kBytes);
+    return wide ? prepare_rows_kernel<D, 2>() : prepare_rows_kernel<D, 1>();
   }
-  if (wide) launch_rows_kernel<D, 2>(rp, mk, mv, st);
-  else launch_rows_kernel<D, 1>(rp, mk, mv, st);
   if (tiles)
     launch_pdl(paged::tile_kernel<D>, dim3(paged::kSMs), dim3(paged::kTileThreads), paged::TileSmem<D>::kBytes, st,
-               mq, mk128, mv128, tp);
-  const unsigned cuts = tiles ? (paged::kSMs - 1) * (256 / paged::kJoinWarps) : 0;
-  launch_pdl(paged::join_kernel<D>, dim3(static_cast<unsigned>(rp.v.B) * rp.v.Hk + cuts),
-             dim3(32 * paged::kJoinWarps), 0, st, jp);
+               mq, mk, mv, tp);
+  else if (wide)
+    launch_rows_kernel<D, 2>(rp, mk, mv, st);
+  else
+    launch_rows_kernel<D, 1>(rp, mk, mv, st);
+  const dim3 grid(tiles ? (paged::kSMs - 1) * (256 / paged::kJoinWarps) : static_cast<unsigned>(rp.v.B) * rp.v.Hk);
+  launch_pdl(tiles ? paged::join_kernel<D, true> : paged::join_kernel<D, false>, grid, dim3(32 * paged::kJoinWarps), 0,
+             st, jp);
   return CSWATTN_OK;
 }
 
@@ -334,10 +335,11 @@ cswattn_status attn_paged(const cswattn_layer* layer, const cswattn_paged* paged
   const PagedWorkspace w = carve_paged(s, v, workspace);
   if (workspace_bytes < w.bytes)
     return fail(CSWATTN_ERR_INVALID_ARG, "paged workspace too small: %zu < %zu bytes", workspace_bytes, w.bytes);
+  const int unit = page_unit(v.page_size, w.tiles ? 128 : paged::kBlk);
   paged::RowsParams rp;
   rp.v = v;
   rp.scale_log2 = s.scale * 1.4426950408889634f;
-  rp.unit = page_unit(v.page_size, paged::kBlk);
+  rp.unit = unit;
   rp.q = static_cast<const __nv_bfloat16*>(q_out);
   rp.O = static_cast<__nv_bfloat16*>(O);
   rp.lse = lse;
@@ -348,44 +350,37 @@ cswattn_status attn_paged(const cswattn_layer* layer, const cswattn_paged* paged
   paged::TileParams tp;
   tp.v = v;
   tp.scale_log2 = rp.scale_log2;
-  tp.unit = page_unit(v.page_size, 128);
+  tp.unit = unit;
   tp.tpt = 128 / s.g;
-  tp.short_rows = w.slot_rows;
   tp.plan = w.plan;
   tp.longs = w.longs;
   tp.O = rp.O;
   tp.lse = lse;
-  tp.part_o = w.tile_o;
-  tp.part_ml = w.tile_ml;
+  tp.part_o = w.part_o;
+  tp.part_ml = w.part_ml;
   tp.wait_ns = rp.wait_ns;
   paged::JoinParams jp;
   jp.v = v;
-  jp.max_rows = w.slot_rows;
+  jp.rows = w.rows;
+  jp.tpt = tp.tpt;
   jp.part_o = w.part_o;
   jp.part_ml = w.part_ml;
   jp.info = w.info;
-  jp.tpt = tp.tpt;
   jp.plan = w.plan;
   jp.longs = w.longs;
-  jp.tile_o = w.tile_o;
-  jp.tile_ml = w.tile_ml;
   jp.O = rp.O;
   jp.lse = lse;
   // What may fail is done before anything is enqueued.
-  CUtensorMap mk, mv, mq, mk128, mv128;
-  if ((st = make_map(&mk, k_pages, v.n_pages, v.page_size, s.Hk, rp.unit, s.D)) != CSWATTN_OK) return st;
-  if ((st = make_map(&mv, v_pages, v.n_pages, v.page_size, s.Hk, rp.unit, s.D)) != CSWATTN_OK) return st;
-  if (w.tiles) {
-    if ((st = make_map_group(&mq, q_out, v.n_tokens, s.H, s.D, s.g, tp.tpt)) != CSWATTN_OK) return st;
-    if ((st = make_map(&mk128, k_pages, v.n_pages, v.page_size, s.Hk, tp.unit, s.D)) != CSWATTN_OK) return st;
-    if ((st = make_map(&mv128, v_pages, v.n_pages, v.page_size, s.Hk, tp.unit, s.D)) != CSWATTN_OK) return st;
-  }
+  CUtensorMap mk, mv, mq;
+  if ((st = make_map(&mk, k_pages, v.n_pages, v.page_size, s.Hk, unit, s.D)) != CSWATTN_OK) return st;
+  if ((st = make_map(&mv, v_pages, v.n_pages, v.page_size, s.Hk, unit, s.D)) != CSWATTN_OK) return st;
+  if (w.tiles && (st = make_map_group(&mq, q_out, v.n_tokens, s.H, s.D, s.g, tp.tpt)) != CSWATTN_OK) return st;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const auto launch = s.D == 64 ? launch_paged<64> : launch_paged<128>;
-  if ((st = launch(rp, tp, jp, w.tiles, mk, mv, mq, mk128, mv128, cs, true)) != CSWATTN_OK) return st;
+  if ((st = launch(rp, tp, jp, w.tiles, mk, mv, mq, cs, true)) != CSWATTN_OK) return st;
   {
     ScopedTiming tm(CSWATTN_K_DECODE, cs);
-    launch(rp, tp, jp, w.tiles, mk, mv, mq, mk128, mv128, cs, false);
+    launch(rp, tp, jp, w.tiles, mk, mv, mq, cs, false);
   }
   return launched("paged attention launch");
 }

@@ -38,7 +38,6 @@ struct TileParams {
   float scale_log2;
   int unit;        // rows of a K or V box
   int tpt;         // tokens per tile: 128 / g
-  int short_rows;  // sequences with more query rows than this are this kernel's
   Plan* plan;
   int* longs;
   __nv_bfloat16* O;
@@ -114,7 +113,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   __shared__ Run run;
   static_assert(kPlanSmem <= SM::kOffBar, "the plan's scratch lies where the tiles will");
   pdl_wait();
-  find_run(v, TokenUnits{p.tpt}, p.short_rows, gridDim.x, c, p.plan, p.longs, smem, &run);
+  find_run(v, TokenUnits{p.tpt}, 0, gridDim.x, c, p.plan, p.longs, smem, &run);
   if (run.left == 0) return;  // uniform over the CTA, before TMEM is taken
   fence_proxy_async_smem();   // the scratch is written, the copies of the tiles come next
   if (warp == 1) {
@@ -454,17 +453,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
 struct JoinParams {
   View v;
-  // pairs that rows_kernel cut
-  int max_rows;       // query rows of a slot
+  int rows, tpt;     // query rows of a share; tokens of a tile
   const float* part_o;
   const float2* part_ml;
-  const int2* info;
-  // units that tile_kernel cut
-  int tpt;
-  const Plan* plan;
+  const int2* info;  // of rows_kernel
+  const Plan* plan;  // of tile_kernel
   const int* longs;
-  const float* tile_o;
-  const float2* tile_ml;
   __nv_bfloat16* O;
   float* lse;
 };
@@ -505,41 +499,41 @@ __device__ __forceinline__ void join_row(const float* part_o, const float2* part
   if (lane == 0) *lse = (M + log2f(L)) * 0.69314718055994531f;
 }
 
-// CTAs [0, B Hk): a (sequence, KV head) pair that rows_kernel cut. The CTAs
-// behind them: a boundary between two CTAs' runs of tile_kernel and 8 of the
-// 256 rows of the unit cut there.
-template <int D>
+// CTA = a (sequence, KV head) pair, joined if rows_kernel cut it; or, with
+// TILES, a boundary between two CTAs' runs of tile_kernel and 8 of the 256
+// rows of the unit cut there.
+template <int D, bool TILES>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const JoinParams p) {
   pdl_launch_dependents();
   pdl_wait();
   const View& v = p.v;
   Seq s{};
   auto out_row = [&](int hk, int i, int h) { return static_cast<size_t>(s.tok0 + i) * v.H + hk * v.g + h; };
-  const int pairs = v.B * v.Hk;
-  if (static_cast<int>(blockIdx.x) < pairs) {
+  if constexpr (!TILES) {
     const int b = blockIdx.x / v.Hk, hk = blockIdx.x % v.Hk;
-    const int2 inf = p.info[blockIdx.x];  // unspecified for a sequence that is not rows_kernel's
+    const int2 inf = p.info[blockIdx.x];  // unspecified for a sequence without tokens
     int first;
     seq_load(v, b, false, s);
-    if (visible_blocks(v, s, p.max_rows, first) == 0 || inf.y <= 1) return;
+    if (visible_blocks(v, s, p.rows, first) == 0 || inf.y <= 1) return;
     for (int r = warp_id(); r < s.n * v.g; r += kJoinWarps) {
       const size_t row = out_row(hk, r / v.g, r % v.g);
       join_row<D>(p.part_o, p.part_ml, inf.y,
-                  [&](int k) { return static_cast<size_t>(k == 0 ? inf.x : 2 * ((inf.x >> 1) + k)) * p.max_rows + r; },
+                  [&](int k) { return static_cast<size_t>(k == 0 ? inf.x : 2 * ((inf.x >> 1) + k)) * p.rows + r; },
                   p.O + row * D, p.lse + row);
     }
-    return;
+  } else {
+    const int x = blockIdx.x;
+    Cut cut;
+    if (!cut.find(p.plan, x / (256 / kJoinWarps) + 1)) return;
+    seq_load(v, p.longs[cut.st.k], false, s);
+    const int row = x % (256 / kJoinWarps) * kJoinWarps + warp_id();  // of the unit's two tiles
+    const int r = row & 127, i = (2 * cut.st.unit + (row >> 7)) * p.tpt + r / v.g;
+    if (r >= p.tpt * v.g || i >= s.n) return;
+    const size_t o = out_row(cut.st.hk, i, r % v.g);
+    join_row<D>(p.part_o, p.part_ml, cut.last - cut.c + 2,
+                [&](int k) { return static_cast<size_t>(cut.slot(cut.c - 1 + k)) * 256 + row; }, p.O + o * D,
+                p.lse + o);
   }
-  const int x = blockIdx.x - pairs;
-  Cut cut;
-  if (!cut.find(p.plan, x / (256 / kJoinWarps) + 1)) return;
-  seq_load(v, p.longs[cut.st.k], false, s);
-  const int row = x % (256 / kJoinWarps) * kJoinWarps + warp_id();  // of the unit's two tiles
-  const int r = row & 127, i = (2 * cut.st.unit + (row >> 7)) * p.tpt + r / v.g;
-  if (r >= p.tpt * v.g || i >= s.n) return;
-  const size_t o = out_row(cut.st.hk, i, r % v.g);
-  join_row<D>(p.tile_o, p.tile_ml, cut.last - cut.c + 2,
-              [&](int k) { return static_cast<size_t>(cut.slot(cut.c - 1 + k)) * 256 + row; }, p.O + o * D, p.lse + o);
 }
 
 }  // namespace paged
