@@ -85,7 +85,7 @@ struct PagedWorkspace {
   float2* part_ml;
   int2* info;          // rows_kernel: the pairs' shares
   paged::Plan* plan;   // tile_kernel: the CTAs' runs, and the sequences in order
-  int* longs;
+  int* seqs;
   size_t bytes;
 };
 
@@ -106,10 +106,10 @@ PagedWorkspace carve_paged(const Shape& s, const paged::View& v, void* base) {
   w.part_ml = static_cast<float2*>(take(rows * 8));
   w.info = nullptr;
   w.plan = nullptr;
-  w.longs = nullptr;
+  w.seqs = nullptr;
   if (w.tiles) {
     w.plan = static_cast<paged::Plan*>(take(sizeof(paged::Plan)));
-    w.longs = static_cast<int*>(take(static_cast<size_t>(s.B) * 4));
+    w.seqs = static_cast<int*>(take(static_cast<size_t>(s.B) * 4));
   } else {
     w.info = static_cast<int2*>(take(static_cast<size_t>(s.B) * s.Hk * 8));
   }
@@ -172,13 +172,19 @@ cswattn_status launch_paged(const paged::RowsParams& rp, const paged::TileParams
 
 struct WeighWorkspace {
   paged::Plan* plan;
-  int* longs;
+  int* seqs;
   float* part;
   int max_rows;  // query rows of a sequence that the kernel of few takes
   bool tiles;    // a sequence may have more
   size_t bytes;
 };
 
+// A call whose sequences have at most 32 query rows (new tokens x heads of a
+// group) runs weigh_rows_kernel, one with more runs weigh_tile_kernel for all
+// of its sequences, single tokens too. Both launched, each for its sequences,
+// is the slower for 31 single tokens over 2000 rows beside a chunk of 512
+// tokens (38.2 us, 36.3) and for 8 sequences of 64 tokens (12.8, 10.8), the
+// faster for 63 single tokens over 4000 rows beside a chunk of 64 (79.9, 90.6).
 WeighWorkspace carve_weigh(const Shape& s, const paged::View& v, void* base) {
   uint8_t* p = static_cast<uint8_t*>(base);
   WeighWorkspace w;
@@ -186,14 +192,14 @@ WeighWorkspace carve_weigh(const Shape& s, const paged::View& v, void* base) {
   w.max_rows = rows <= 8 ? 8 : (rows <= 16 ? 16 : 32);
   w.tiles = rows > w.max_rows;
   w.plan = nullptr;
-  w.longs = nullptr;
+  w.seqs = nullptr;
   w.part = nullptr;
   w.bytes = 0;
   if (!w.tiles) return w;
   size_t off = 0;
   w.plan = reinterpret_cast<paged::Plan*>(p + off);
   off += pad256(sizeof(paged::Plan));
-  w.longs = reinterpret_cast<int*>(p + off);
+  w.seqs = reinterpret_cast<int*>(p + off);
   off += pad256(static_cast<size_t>(s.B) * 4);
   w.part = reinterpret_cast<float*>(p + off);
   off += pad256(static_cast<size_t>(2 * paged::kWeighRuns) * 128 * 4);
@@ -214,15 +220,14 @@ cswattn_status launch_weigh_rows(const paged::WeighRowsParams& rp, const CUtenso
 // As launch_paged, for the row weights.
 template <int D>
 cswattn_status launch_weigh(const paged::WeighRowsParams& rp, const paged::WeighTileParams& tp, bool tiles,
-                            const CUtensorMap& mk, const CUtensorMap& mq, const CUtensorMap& mk128, cudaStream_t st,
-                            bool prepare_only) {
-  cswattn_status e = rp.max_rows == 8    ? launch_weigh_rows<D, 1>(rp, mk, st, prepare_only)
-                     : rp.max_rows == 16 ? launch_weigh_rows<D, 2>(rp, mk, st, prepare_only)
-                                         : launch_weigh_rows<D, 4>(rp, mk, st, prepare_only);
-  if (e != CSWATTN_OK || !tiles) return e;
+                            const CUtensorMap& mk, const CUtensorMap& mq, cudaStream_t st, bool prepare_only) {
+  if (!tiles)
+    return rp.max_rows == 8    ? launch_weigh_rows<D, 1>(rp, mk, st, prepare_only)
+           : rp.max_rows == 16 ? launch_weigh_rows<D, 2>(rp, mk, st, prepare_only)
+                               : launch_weigh_rows<D, 4>(rp, mk, st, prepare_only);
   if (prepare_only) return set_smem(paged::weigh_tile_kernel<D>, paged::WeighTileSmem<D>::kBytes);
   launch_pdl(paged::weigh_tile_kernel<D>, dim3(paged::kWeighRuns), dim3(paged::kWeighThreads),
-             paged::WeighTileSmem<D>::kBytes, st, mq, mk128, tp);
+             paged::WeighTileSmem<D>::kBytes, st, mq, mk, tp);
   launch_pdl(paged::weigh_join_kernel, dim3(paged::kWeighRuns - 1), dim3(128), 0, st, tp);
   return CSWATTN_OK;
 }
@@ -353,7 +358,7 @@ cswattn_status attn_paged(const cswattn_layer* layer, const cswattn_paged* paged
   tp.unit = unit;
   tp.tpt = 128 / s.g;
   tp.plan = w.plan;
-  tp.longs = w.longs;
+  tp.seqs = w.seqs;
   tp.O = rp.O;
   tp.lse = lse;
   tp.part_o = w.part_o;
@@ -367,7 +372,7 @@ cswattn_status attn_paged(const cswattn_layer* layer, const cswattn_paged* paged
   jp.part_ml = w.part_ml;
   jp.info = w.info;
   jp.plan = w.plan;
-  jp.longs = w.longs;
+  jp.seqs = w.seqs;
   jp.O = rp.O;
   jp.lse = lse;
   // What may fail is done before anything is enqueued.
@@ -412,7 +417,7 @@ cswattn_status attn_paged_weigh(const cswattn_layer* layer, const cswattn_paged*
   paged::WeighRowsParams rp;
   rp.v = v;
   rp.scale_log2 = s.scale * 1.4426950408889634f;
-  rp.unit = page_unit(v.page_size, paged::kBlk);
+  rp.unit = page_unit(v.page_size, w.tiles ? 128 : paged::kBlk);
   rp.max_rows = w.max_rows;
   rp.q = static_cast<const __nv_bfloat16*>(q_out);
   rp.lse = lse;
@@ -421,27 +426,23 @@ cswattn_status attn_paged_weigh(const cswattn_layer* layer, const cswattn_paged*
   paged::WeighTileParams tp;
   tp.v = v;
   tp.scale_log2 = rp.scale_log2;
-  tp.unit = page_unit(v.page_size, 128);
+  tp.unit = rp.unit;
   tp.tpt = 128 / s.g;
-  tp.short_rows = w.max_rows;
   tp.plan = w.plan;
-  tp.longs = w.longs;
+  tp.seqs = w.seqs;
   tp.lse = lse;
   tp.weight = weight;
   tp.part = w.part;
   tp.wait_ns = rp.wait_ns;
-  CUtensorMap mk, mq, mk128;
+  CUtensorMap mk, mq;
   if ((st = make_map(&mk, k_pages, v.n_pages, v.page_size, s.Hk, rp.unit, s.D)) != CSWATTN_OK) return st;
-  if (w.tiles) {
-    if ((st = make_map_group(&mq, q_out, v.n_tokens, s.H, s.D, s.g, tp.tpt)) != CSWATTN_OK) return st;
-    if ((st = make_map(&mk128, k_pages, v.n_pages, v.page_size, s.Hk, tp.unit, s.D)) != CSWATTN_OK) return st;
-  }
+  if (w.tiles && (st = make_map_group(&mq, q_out, v.n_tokens, s.H, s.D, s.g, tp.tpt)) != CSWATTN_OK) return st;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const auto launch = s.D == 64 ? launch_weigh<64> : launch_weigh<128>;
-  if ((st = launch(rp, tp, w.tiles, mk, mq, mk128, cs, true)) != CSWATTN_OK) return st;
+  if ((st = launch(rp, tp, w.tiles, mk, mq, cs, true)) != CSWATTN_OK) return st;
   {
     ScopedTiming tm(CSWATTN_K_DECODE, cs);
-    launch(rp, tp, w.tiles, mk, mq, mk128, cs, false);
+    launch(rp, tp, w.tiles, mk, mq, cs, false);
   }
   return launched("paged weights launch");
 }

@@ -1,6 +1,6 @@
-// paged_plan.cuh -- how work on many query rows is dealt out. A long sequence
-// is a row of units per KV head, each of some blocks; the units of all long
-// sequences follow one another, and CTA c of n takes the blocks
+// paged_plan.cuh -- how work on many query rows is dealt out. A sequence that
+// has new tokens is a row of units per KV head, each of some blocks; the units
+// of all of them follow one another, and CTA c of n takes the blocks
 // [total c / n, total (c + 1) / n): whole units, and at most two cut ones.
 // Each CTA finds its own run (find_run: all its threads add up the units of
 // all sequences, which is quicker than a launch that does it for everybody)
@@ -23,7 +23,7 @@ __device__ __forceinline__ long long share_of(long long total, int c, int n) {
   return total * c / n;
 }
 
-// Where a CTA's run starts: the k-th long sequence, KV head, unit, block of the unit.
+// Where a CTA's run starts: the k-th sequence that has tokens, KV head, unit, block of the unit.
 struct Start {
   int k, hk, unit, t0;
 };
@@ -39,11 +39,6 @@ struct Run {
   long long left;
   Seq s;
 };
-
-// Sequences with more query rows (new tokens x heads of a group) than short_rows.
-__device__ __forceinline__ bool is_long(const View& v, const Seq& s, int short_rows) {
-  return static_cast<long long>(s.n) * v.g > short_rows;
-}
 
 // Tiles of 128 cached rows that the tokens [i0, i1) of a sequence see.
 __device__ __forceinline__ void token_blocks(const View& v, const Seq& s, int i0, int i1, int& lo, int& hi) {
@@ -82,12 +77,13 @@ struct RowUnits {
 constexpr int kPlanSmem = 8 * (kMaxSeqs + 1) + 4 * 36;
 
 // All threads of a CTA (a multiple of 32, at most 1024) call; `smem` is
-// kPlanSmem bytes of scratch; `longs` (the long sequences, in order) is written
-// alike by every CTA. The result is in *run, in shared memory.
+// kPlanSmem bytes of scratch; `seqs` (the sequences that have tokens, in
+// order) is written alike by every CTA. The result is in *run, in shared
+// memory.
 template <class Units>
-__device__ __forceinline__ void find_run(const View& v, const Units& units, int short_rows, int runs, int c, Plan* plan,
-                                         int* longs, void* smem, Run* run) {
-  long long* pre = static_cast<long long*>(smem);  // per long sequence: blocks of one KV head before it
+__device__ __forceinline__ void find_run(const View& v, const Units& units, int runs, int c, Plan* plan,
+                                         int* seqs, void* smem, Run* run) {
+  long long* pre = static_cast<long long*>(smem);  // per such sequence: blocks of one KV head before it
   int* s_total = reinterpret_cast<int*>(pre + kMaxSeqs + 1);
   const int warp = warp_id(), lane = lane_id(), warps = blockDim.x >> 5;
   auto blocks = [&](const Seq& s, int u) -> int {
@@ -95,23 +91,23 @@ __device__ __forceinline__ void find_run(const View& v, const Units& units, int 
     units.range(v, s, u, lo, hi);
     return hi - lo + 1;
   };
-  int n_long = 0;
+  int n_seqs = 0;
   for (int b0 = 0; b0 < v.B; b0 += blockDim.x) {
     const int b = b0 + threadIdx.x;
     bool yes = false;
     Seq s;
-    if (b < v.B) yes = seq_load(v, b, c == 0, s) && is_long(v, s, short_rows);
+    if (b < v.B) yes = seq_load(v, b, c == 0, s) && s.n > 0;
     const uint32_t m = __ballot_sync(0xffffffffu, yes);
     if (lane == 0) s_total[warp] = __popc(m);
     __syncthreads();
-    int before = n_long;
+    int before = n_seqs;
     for (int w = 0; w < warps; ++w) {
       if (w < warp) before += s_total[w];
-      n_long += s_total[w];
+      n_seqs += s_total[w];
     }
     if (yes) {
       const int k = before + __popc(m & ((1u << lane) - 1u)), n = units.count(v, s);
-      longs[k] = b;
+      seqs[k] = b;
       long long sum = -1;  // few units: this thread adds them up; else a warp does
       if (n <= 8) {
         sum = 0;
@@ -121,10 +117,10 @@ __device__ __forceinline__ void find_run(const View& v, const Units& units, int 
     }
     __syncthreads();
   }
-  for (int k = warp; k < n_long; k += warps) {
+  for (int k = warp; k < n_seqs; k += warps) {
     if (pre[k + 1] >= 0) continue;
     Seq s;
-    seq_load(v, longs[k], false, s);
+    seq_load(v, seqs[k], false, s);
     const int n = units.count(v, s);
     long long sum = 0;
     for (int u = lane; u < n; u += 32) sum += blocks(s, u);
@@ -140,14 +136,14 @@ __device__ __forceinline__ void find_run(const View& v, const Units& units, int 
   __syncthreads();
   if (warp == 0) {
     long long sum = 0;
-    for (int k0 = 0; k0 < n_long; k0 += 32) {
-      long long x = k0 + lane < n_long ? pre[k0 + lane + 1] : 0;
+    for (int k0 = 0; k0 < n_seqs; k0 += 32) {
+      long long x = k0 + lane < n_seqs ? pre[k0 + lane + 1] : 0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const long long y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
       }
-      if (k0 + lane < n_long) pre[k0 + lane + 1] = sum + x;
+      if (k0 + lane < n_seqs) pre[k0 + lane + 1] = sum + x;
       sum += __shfl_sync(0xffffffffu, x, 31);
     }
     __syncwarp();
@@ -157,14 +153,14 @@ __device__ __forceinline__ void find_run(const View& v, const Units& units, int 
     if (c == 0 && lane == 0) plan->ctas = ctas;
     if (c < ctas) {
       const long long at = share_of(total, c, ctas);
-      int lo = 0, hi = n_long;  // the last k with pre[k] * Hk <= at
+      int lo = 0, hi = n_seqs;  // the last k with pre[k] * Hk <= at
       while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
         if (pre[mid] * v.Hk <= at) lo = mid;
         else hi = mid;
       }
       Seq s;
-      seq_load(v, longs[lo], false, s);
+      seq_load(v, seqs[lo], false, s);
       const long long cnt = pre[lo + 1] - pre[lo], rem = at - pre[lo] * v.Hk;
       long long left = rem % cnt;
       const int n = units.count(v, s);
@@ -198,19 +194,19 @@ template <class Units>
 struct UnitWalk {
   const View& v;
   const Units units;
-  const int* longs;
+  const int* seqs;
   long long left;
   int k, hk, u, t0, t1, cnt, n_units, first;
   Seq s;
-  __device__ UnitWalk(const View& v_, const Units& units_, const Run& run, const int* longs_)
-      : v(v_), units(units_), longs(longs_), left(run.left), k(run.st.k), hk(run.st.hk), u(run.st.unit), t0(run.st.t0),
+  __device__ UnitWalk(const View& v_, const Units& units_, const Run& run, const int* seqs_)
+      : v(v_), units(units_), seqs(seqs_), left(run.left), k(run.st.k), hk(run.st.hk), u(run.st.unit), t0(run.st.t0),
         s(run.s) {
     n_units = units.count(v, s);
     set();
   }
-  __device__ int seq() const { return longs[k]; }
+  __device__ int seq() const { return seqs[k]; }
   __device__ void load() {
-    seq_load(v, longs[k], false, s);
+    seq_load(v, seqs[k], false, s);
     n_units = units.count(v, s);
   }
   __device__ void set() {

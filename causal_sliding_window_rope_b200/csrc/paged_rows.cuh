@@ -1,14 +1,18 @@
-// paged_rows.cuh -- paged attention of sequences with few query rows (new
-// tokens x heads of a group at most 16 MB): a generation step, a few
+// paged_rows.cuh -- paged attention of calls with few query rows a sequence
+// (new tokens x heads of a group at most 16 MB): a generation step, a few
 // speculated tokens. The step reads every visible K and V row once, so it is
-// bound by HBM; the products need 16 x 8 tiles, not 128 x 128 ones.
+// bound by HBM; the products need 16 x 8 tiles, not 128 x 128 ones. Measured
+// with its join: 32 sequences of 2048 rows, 12 heads on 4 of 128, 28.0 us =
+// 4.8 TB/s (0.73 of a copy's rate), about 3 us of it the CTAs' start (lengths,
+// page table, first copy: dependent loads) and 3 the launches; one sequence of
+// 1000 rows, 6 heads, 9.8 us.
 //
 // Work is cut by bytes, not by sequence: the 64-row blocks of all (sequence,
 // KV head) pairs in a row are dealt out evenly to one CTA per SM, so ragged
 // lengths and any number of sequences load the SMs alike. A CTA's run covers
 // whole pairs, whose output it writes itself, and at most two cut ones (its
 // first and its last), whose partial maximum, sum and float32 output go to
-// the workspace; combine_kernel joins those.
+// the workspace; join_kernel joins those.
 //
 // CTA: one producer warp streams 64-row blocks of K and V through a ring (one
 // TMA box per page unit and 64-column panel, 128B swizzle, straight on from

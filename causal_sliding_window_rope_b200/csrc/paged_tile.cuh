@@ -1,5 +1,5 @@
-// paged_tile.cuh -- paged attention of sequences with many query rows (a
-// prompt's chunk): tcgen05 tensor cores, 128-row tiles.
+// paged_tile.cuh -- paged attention of calls in which some sequence has many
+// query rows (a prompt's chunk): tcgen05 tensor cores, 128-row tiles.
 //
 // A tile's 128 rows are tokens x heads of one KV head's group (row = token in
 // the tile * g + head in the group; 128 / g tokens), so every head that reads
@@ -15,14 +15,18 @@
 //               one 5-slot ring; every lane copies one box (a page unit of
 //               rows x 64 columns); units that no token sees are read past the
 //               pool's end, which fills zeros
-//   warp 1      TMEM owner, single-thread MMA issuer
+//   warp 1      TMEM owner, MMA issuer
 //   warps 4-7   softmax of tile 0, warps 8-11 of tile 1: thread = query row
 // TMEM (512 columns): S0 | S1 | O0 | O1. Per block: S = Q K^T, P (bf16) over
 // the S columns, O += P V, in the order PV_0(j), S_0(j+1), PV_1(j), S_1(j+1)
 // so that one tile's softmax overlaps the other's products. The barriers'
 // phases run on from unit to unit, and the next unit's first S is issued
 // while the last one's output is still being written.
-// Bound by the softmax (one exponential per score) and the tensor pipe.
+// Bound by the chain of a tile (S, softmax, P V, next S: about 3200 cycles a
+// block, the products 2050 of them) and, in long runs, by the power limit
+// (1.6 GHz): 2 x 2048 tokens of 16 heads on 4 over 8192 rows 253 us = 951
+// TFLOP/s (0.58 of the burst, 0.68 of the sustained rate of a matrix product).
+// Two warps that issue, one per tile, let the tiles fall into step: 302 us.
 #pragma once
 #include "paged_rows.cuh"
 
@@ -39,7 +43,7 @@ struct TileParams {
   int unit;        // rows of a K or V box
   int tpt;         // tokens per tile: 128 / g
   Plan* plan;
-  int* longs;
+  int* seqs;
   __nv_bfloat16* O;
   float* lse;
   float* part_o;     // (2 kSMs, 256, D)
@@ -50,7 +54,7 @@ struct TileParams {
 // The walk, with the blocks [lo, hi] of the segment that tile X (0 or 1) of the unit has.
 struct TileWalk : UnitWalk<TokenUnits> {
   __device__ TileWalk(const TileParams& p, const Run& run)
-      : UnitWalk<TokenUnits>(p.v, TokenUnits{p.tpt}, run, p.longs) {}
+      : UnitWalk<TokenUnits>(p.v, TokenUnits{p.tpt}, run, p.seqs) {}
   __device__ bool tokens(int X) const { return (2 * u + X) * units.tpt < s.n; }
   __device__ bool tile(int X, int& lo, int& hi) const {
     const int i0 = (2 * u + X) * units.tpt;
@@ -113,7 +117,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   __shared__ Run run;
   static_assert(kPlanSmem <= SM::kOffBar, "the plan's scratch lies where the tiles will");
   pdl_wait();
-  find_run(v, TokenUnits{p.tpt}, 0, gridDim.x, c, p.plan, p.longs, smem, &run);
+  find_run(v, TokenUnits{p.tpt}, gridDim.x, c, p.plan, p.seqs, smem, &run);
   if (run.left == 0) return;  // uniform over the CTA, before TMEM is taken
   fence_proxy_async_smem();   // the scratch is written, the copies of the tiles come next
   if (warp == 1) {
@@ -458,7 +462,7 @@ struct JoinParams {
   const float2* part_ml;
   const int2* info;  // of rows_kernel
   const Plan* plan;  // of tile_kernel
-  const int* longs;
+  const int* seqs;
   __nv_bfloat16* O;
   float* lse;
 };
@@ -525,7 +529,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const JoinParams 
     const int x = blockIdx.x;
     Cut cut;
     if (!cut.find(p.plan, x / (256 / kJoinWarps) + 1)) return;
-    seq_load(v, p.longs[cut.st.k], false, s);
+    seq_load(v, p.seqs[cut.st.k], false, s);
     const int row = x % (256 / kJoinWarps) * kJoinWarps + warp_id();  // of the unit's two tiles
     const int r = row & 127, i = (2 * cut.st.unit + (row >> 7)) * p.tpt + r / v.g;
     if (r >= p.tpt * v.g || i >= s.n) return;

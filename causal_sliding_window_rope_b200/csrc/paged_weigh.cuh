@@ -4,16 +4,21 @@
 //
 // The sums run over queries, so the products are taken transposed (a cached
 // row is a row of S^T = K Q^T) and each sum stays inside one thread, or four
-// lanes. Every cached row belongs to one CTA (or one cluster) of a call, which
-// adds in a fixed order and updates the row without atomics: the same call
-// gives the same bits.
+// lanes. Every cached row belongs to one CTA of a call (the shares of a unit
+// that is cut are added by a kernel of their own), which adds in a fixed order
+// and updates the row without atomics: the same call gives the same bits.
 //
-// Two kernels, by a sequence's query rows (new tokens x heads of the group):
-//   weigh_rows_kernel   few rows (<= 32): bound by reading K once. Blocks of 64
-//     cached rows, dealt out evenly as in the attention of few rows; mma.sync
-//     with K as the first operand, the query rows as columns (8 per product).
-//   weigh_tile_kernel   many rows: tcgen05, 128 cached rows x 128 query rows
-//     per product, thread = cached row; bound by the exponentials.
+// Two kernels, by the most query rows a sequence of the call may have (new
+// tokens x heads of the group):
+//   weigh_rows_kernel   few (<= 32): bound by reading K once and by the start
+//     of a CTA. Blocks of 64 cached rows, dealt out evenly as in the attention
+//     of few rows; mma.sync with K as the first operand, the query rows as
+//     columns (8 per product). 32 ragged sequences of up to 2048 rows 12.8 us.
+//   weigh_tile_kernel   many: tcgen05, 128 cached rows x 128 query rows per
+//     product, two threads per cached row; bound by the exponentials (one per
+//     score on the MUFU unit, 57 % busy). 2213 tokens of 16 heads on 4 over
+//     11081 rows 65 us = 520 TFLOP/s.A call with a chunk runs it for its
+//     single tokens too.
 #pragma once
 #include "paged_tile.cuh"
 
@@ -214,9 +219,9 @@ __global__ void __launch_bounds__(32 * (4 * WeighGroups<NT>::value + 1), 1)
 struct WeighTileParams {
   View v;
   float scale_log2;
-  int unit, tpt, short_rows;
+  int unit, tpt;
   Plan* plan;
-  int* longs;
+  int* seqs;
   const float* lse;
   float* weight;
   float* part;  // (2 kWeighRuns, 128): sums of cut units
@@ -287,7 +292,7 @@ __global__ void __launch_bounds__(kWeighThreads, 2)
   __shared__ Run run;
   static_assert(kPlanSmem <= SM::kOffTerm, "the plan's scratch lies where the tiles will");
   pdl_wait();
-  find_run(v, RowUnits{p.tpt}, p.short_rows, gridDim.x, c, p.plan, p.longs, smem, &run);
+  find_run(v, RowUnits{p.tpt}, gridDim.x, c, p.plan, p.seqs, smem, &run);
   if (run.left == 0) return;  // uniform over the CTA, before TMEM is taken
   fence_proxy_async_smem();   // the scratch is written, the copies of the tiles come next
   if (warp == 1) {
@@ -299,7 +304,7 @@ __global__ void __launch_bounds__(kWeighThreads, 2)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const WaitCtx wc{abort_flag, p.wait_ns};
-  UnitWalk<RowUnits> w(v, RowUnits{p.tpt}, run, p.longs);
+  UnitWalk<RowUnits> w(v, RowUnits{p.tpt}, run, p.seqs);
   bool ok = true;
 
   if (warp == 0) {
@@ -500,7 +505,7 @@ __global__ void __launch_bounds__(128) weigh_join_kernel(const __grid_constant__
   Cut cut;
   if (!cut.find(p.plan, blockIdx.x + 1)) return;
   const View& v = p.v;
-  const int b = p.longs[cut.st.k];
+  const int b = p.seqs[cut.st.k];
   Seq s;
   seq_load(v, b, false, s);
   const int key = RowUnits{p.tpt}.first_row(v, s, cut.st.unit) + threadIdx.x;
