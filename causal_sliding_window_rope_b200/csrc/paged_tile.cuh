@@ -515,10 +515,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const JoinParams 
   auto out_row = [&](int hk, int i, int h) { return static_cast<size_t>(s.tok0 + i) * v.H + hk * v.g + h; };
   if constexpr (!TILES) {
     const int b = blockIdx.x / v.Hk, hk = blockIdx.x % v.Hk;
-    const int2 inf = p.info[blockIdx.x];  // unspecified for a sequence without tokens
+    // Unspecified for a sequence without tokens, and where a wait of
+    // rows_kernel has run out: what does not name slots is not followed.
+    const int2 inf = p.info[blockIdx.x];
     int first;
     seq_load(v, b, false, s);
     if (visible_blocks(v, s, p.rows, first) == 0 || inf.y <= 1) return;
+    if (inf.x < 0 || inf.x >= 2 * kSMs || inf.y > kSMs - (inf.x >> 1)) return;
     for (int r = warp_id(); r < s.n * v.g; r += kJoinWarps) {
       const size_t row = out_row(hk, r / v.g, r % v.g);
       join_row<D>(p.part_o, p.part_ml, inf.y,
