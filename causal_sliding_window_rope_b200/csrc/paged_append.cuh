@@ -15,13 +15,12 @@
 // heads 28.9 us = 3.8 TB/s (a copy of a kernel this short reaches 4.5); 25
 // tokens 7.4 us. Staging the tokens in shared memory by bulk copies took 33.8
 // us, holding rows in registers ahead of the setup 30 to 41: both cost CTAs in
-// flight. A CTA takes kAppendTok
-// consecutive tokens: its threads find the tokens' sequences by one coalesced
-// pass over new_start, fill a cos/sin table, then walk the rows. A row of D
-// elements belongs to D / 16 lanes, 16 elements each as two 16-byte vectors:
-// with the half layout lane l < R/16 holds [8l, 8l + 8) of both halves of the
-// rotary part, so each pair is inside one lane; all others hold 16
-// consecutive elements.
+// flight. A CTA takes kAppendTok consecutive tokens: its threads find the
+// tokens' sequences by one coalesced pass over new_start, fill a cos/sin table,
+// then walk the rows. A row of D elements belongs to D / 16 lanes, 16 elements
+// each as two 16-byte vectors: with the half layout lane l < R/16 holds
+// [8l, 8l + 8) of both halves of the rotary part, so each pair is inside one
+// lane; all others hold 16 consecutive elements.
 #pragma once
 #include "paged.cuh"
 

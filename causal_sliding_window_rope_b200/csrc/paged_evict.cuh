@@ -66,7 +66,8 @@ __device__ __forceinline__ uint2 peer_load2(const void* p, int rank) {
 // others have to know of a CTA's rows is exchanged once. Every path of a
 // cluster's CTAs meets the same barriers. Measured: 128 heads of 1025 rows 8.5
 // us; 16 heads of up to 40000 rows 22.2 us (111 with one CTA a head).
-// A lone CTA (CLUSTER false) meets itself at the block's barrier and reads its own counts.
+// A lone CTA (CLUSTER false) meets itself at the block's barrier and reads its
+// own counts.
 template <bool CLUSTER>
 __global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectParams p) {
   const int ranks = CLUSTER ? gridDim.x : 1;
@@ -337,9 +338,9 @@ constexpr int kMoveBatch = 4;        // moves a group of lanes has in flight
 // The rows lie anywhere, so what counts is how many loads are in flight. A
 // CTA takes kMoveThreads moves at a time (67 thousand rows of 16 sequences
 // 19.4 us = 3.6 TB/s, and 25 with a group of lanes per move all the way):
-// first a thread per move follows
-// move and page to the two rows' places (three dependent loads, paid once),
-// then D / 8 lanes copy a row of K and of V, kMoveBatch moves at a time.
+// first a thread per move follows move and page to the two rows' places (three
+// dependent loads, paid once), then D / 8 lanes copy a row of K and of V,
+// kMoveBatch moves at a time.
 template <int D>
 __global__ void __launch_bounds__(kMoveThreads, 4) move_kernel(const MoveParams p) {
   constexpr int LPR = D / 8, GPC = kMoveThreads / LPR;
@@ -349,12 +350,12 @@ __global__ void __launch_bounds__(kMoveThreads, 4) move_kernel(const MoveParams 
   pdl_launch_dependents();
   pdl_wait();
   const size_t head = static_cast<size_t>(b) * v.Hk + hk;
-  const int n = p.n_moves[head];
+  const int n = p.n_moves[head], L = v.cache_len[b];
   for (int i0 = blockIdx.x * kMoveThreads; i0 < p.stride; i0 += gridDim.x * kMoveThreads) {
     const bool in = i0 + tid < p.stride;
     const int from = in ? p.src[head * p.stride + i0 + tid] : 0;  // (beside n: one latency less)
     const int to = in ? p.dst[head * p.stride + i0 + tid] : 0;
-    if (n < 0 || n > p.stride) {
+    if (n < 0 || n > p.stride || L < 0 || L > v.T) {  // (select writes nothing for a length that does not fit)
       if (blockIdx.x == 0 && tid == 0) atomicOr(&g_status, kStatusRange);
       return;
     }

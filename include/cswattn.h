@@ -374,7 +374,10 @@ size_t attn_paged_workspace_bytes(const cswattn_layer* layer, const cswattn_page
  * their rows): O (n_tokens, n_head, head_dim) and lse (n_tokens, n_head),
  * natural log. workspace: at least attn_paged_workspace_bytes, 256-byte
  * aligned; contents on entry do not matter; not to be used by another call in
- * flight. */
+ * flight. What lies in rows that no new token of the sequence sees does not
+ * matter. An infinity or NaN in a row of K reaches the tokens that see the row;
+ * one in a row of V may reach the call's other tokens of that sequence, too (0
+ * times it is NaN), as in attn_fwd. */
 cswattn_status attn_paged(const cswattn_layer* layer, const cswattn_paged* paged, const void* q_out,
                           const void* k_pages, const void* v_pages, void* O, float* lse,
                           void* workspace, size_t workspace_bytes, void* stream);
@@ -414,9 +417,11 @@ cswattn_status attn_paged_select(const cswattn_layer* layer, const cswattn_paged
 
 /* Copies K, V, weight and position of the moved rows (attn_paged_select's
  * n_moves, src, dst with the same n_keep). Sources lie at or past n_keep,
- * targets below it, so the copies are independent of one another. Attention
- * afterwards takes new_len as the cache length; rows are no longer in the
- * order of their positions, so the layer's window should cover all rows. */
+ * targets below it, so the copies are independent of one another. A sequence
+ * whose cache_len does not fit is left untouched here too; pages that move must
+ * not be shared between sequences. Attention afterwards takes new_len as the
+ * cache length; rows are no longer in the order of their positions, so the
+ * layer's window should cover all rows. */
 cswattn_status attn_paged_move(const cswattn_layer* layer, const cswattn_paged* paged, const int* n_moves,
                                const int* src, const int* dst, int n_keep, void* k_pages, void* v_pages,
                                float* weight, int* position, void* stream);

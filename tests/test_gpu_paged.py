@@ -562,6 +562,29 @@ def test_select_length_that_does_not_fit():
     assert int(new_len[1]) == 30 and (n[1] != 99).all()
 
 
+@pytest.mark.parametrize("length", [-1, 101])
+def test_moves_of_a_length_that_does_not_fit(length):
+    # What select has left as it was may hold moves of an earlier call: they are not made.
+    c, w, pos = evict_case([100, 50], 2, 64, 16, None, False, seed=3)
+    batch = c.batch()
+    batch.cache_len[0] = length
+    g = torch.Generator().manual_seed(4)
+    k = torch.randn(c.n_pages, 16, 2, 64, generator=g).to(BF).cuda()
+    cache = cs.PagedCache(c.spec, k=k, v=k.clone(), weight=w.cuda(), position=pos.cuda())
+    i32 = dict(dtype=torch.int32, device="cuda")
+    n, new_len = torch.full((2, 2), 1, **i32), torch.full((2,), 99, **i32)
+    src, dst = torch.full((2, 2, 30), 40, **i32), torch.full((2, 2, 30), 7, **i32)
+    cs.attn_paged_select(c.spec, batch, cache, torch.tensor([200, 100], **i32), 30, 3, n, src, dst, new_len)
+    expect_range_error()
+    k0, w0, p0 = k.clone(), cache.weight.clone(), cache.position.clone()
+    cs.attn_paged_move(c.spec, batch, cache, n, src, dst)
+    expect_range_error()
+    mine = c.table[0].long().cuda()
+    for now, then in ((cache.k, k0), (cache.v, k0), (cache.weight, w0), (cache.position, p0)):
+        assert torch.equal(now[mine], then[mine])
+    assert (n[1] > 0).all() and not torch.equal(cache.k, k0)  # the other sequence's rows did move
+
+
 # ------------------------------------------------------------------ together
 
 class Server:
