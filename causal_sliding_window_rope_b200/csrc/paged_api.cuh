@@ -164,7 +164,7 @@ cswattn_status launch_paged(const paged::RowsParams& rp, const paged::TileParams
     launch_rows_kernel<D, 2>(rp, mk, mv, st);
   else
     launch_rows_kernel<D, 1>(rp, mk, mv, st);
-  const dim3 grid(tiles ? (paged::kSMs - 1) * (256 / paged::kJoinWarps) : static_cast<unsigned>(rp.v.B) * rp.v.Hk);
+  const dim3 grid(tiles ? (paged::kSMs - 1) * paged::kJoinUnitCtas : static_cast<unsigned>(rp.v.B) * rp.v.Hk);
   launch_pdl(tiles ? paged::join_kernel<D, true> : paged::join_kernel<D, false>, grid, dim3(32 * paged::kJoinWarps), 0,
              st, jp);
   return CSWATTN_OK;
@@ -372,7 +372,6 @@ cswattn_status attn_paged(const cswattn_layer* layer, const cswattn_paged* paged
   jp.part_ml = w.part_ml;
   jp.info = w.info;
   jp.plan = w.plan;
-  jp.seqs = w.seqs;
   jp.O = rp.O;
   jp.lse = lse;
   // What may fail is done before anything is enqueued.

@@ -28,9 +28,16 @@ struct Start {
   int k, hk, unit, t0;
 };
 
+// ... and with it what the join needs of the sequence, which is then one load away.
+struct Begin {
+  Start st;
+  Seq s;
+  int b;
+};
+
 struct Plan {
+  Begin begin[kMaxRuns];
   int ctas;
-  Start start[kMaxRuns];
 };
 
 // A CTA's run: `left` blocks from st on (in sequence s); none when left is 0.
@@ -74,7 +81,7 @@ struct RowUnits {
   }
 };
 
-constexpr int kPlanSmem = 8 * (kMaxSeqs + 1) + 4 * 36;
+constexpr int kPlanSmem = 8 * (kMaxSeqs + 1) + 4 * 36 + 2 * kMaxSeqs;
 
 // All threads of a CTA (a multiple of 32, at most 1024) call; `smem` is
 // kPlanSmem bytes of scratch; `seqs` (the sequences that have tokens, in
@@ -85,6 +92,8 @@ __device__ __forceinline__ void find_run(const View& v, const Units& units, int 
                                          int* seqs, void* smem, Run* run) {
   long long* pre = static_cast<long long*>(smem);  // per such sequence: blocks of one KV head before it
   int* s_total = reinterpret_cast<int*>(pre + kMaxSeqs + 1);
+  uint16_t* s_seqs = reinterpret_cast<uint16_t*>(s_total + 36);  // `seqs`, at hand
+  static_assert(kMaxSeqs <= 1 << 16, "sequences in 16 bits");
   const int warp = warp_id(), lane = lane_id(), warps = blockDim.x >> 5;
   auto blocks = [&](const Seq& s, int u) -> int {
     int lo, hi;
@@ -108,6 +117,7 @@ __device__ __forceinline__ void find_run(const View& v, const Units& units, int 
     if (yes) {
       const int k = before + __popc(m & ((1u << lane) - 1u)), n = units.count(v, s);
       seqs[k] = b;
+      s_seqs[k] = static_cast<uint16_t>(b);
       long long sum = -1;  // few units: this thread adds them up; else a warp does
       if (n <= 8) {
         sum = 0;
@@ -120,7 +130,7 @@ __device__ __forceinline__ void find_run(const View& v, const Units& units, int 
   for (int k = warp; k < n_seqs; k += warps) {
     if (pre[k + 1] >= 0) continue;
     Seq s;
-    seq_load(v, seqs[k], false, s);
+    seq_load(v, s_seqs[k], false, s);
     const int n = units.count(v, s);
     long long sum = 0;
     for (int u = lane; u < n; u += 32) sum += blocks(s, u);
@@ -160,9 +170,10 @@ __device__ __forceinline__ void find_run(const View& v, const Units& units, int 
         else hi = mid;
       }
       Seq s;
-      seq_load(v, seqs[lo], false, s);
+      seq_load(v, s_seqs[lo], false, s);
       const long long cnt = pre[lo + 1] - pre[lo], rem = at - pre[lo] * v.Hk;
-      long long left = rem % cnt;
+      const int hk = total < INT_MAX ? static_cast<int>(rem) / static_cast<int>(cnt) : static_cast<int>(rem / cnt);
+      long long left = rem - hk * cnt;
       const int n = units.count(v, s);
       for (int u0 = 0; u0 < n; u0 += 32) {  // 32 units at a time: the one that holds block `left`
         const int u = u0 + lane;
@@ -175,8 +186,8 @@ __device__ __forceinline__ void find_run(const View& v, const Units& units, int 
         }
         const bool here = u < n && left >= inc - mine && left < inc;
         if (here) {
-          const Start st{lo, static_cast<int>(rem / cnt), u, static_cast<int>(left) - (inc - mine)};
-          plan->start[c] = st;
+          const Start st{lo, hk, u, static_cast<int>(left) - (inc - mine)};
+          plan->begin[c] = Begin{st, s, s_seqs[lo]};
           run->st = st;
           run->s = s;
           run->left = share_of(total, c + 1, ctas) - at;
@@ -233,29 +244,53 @@ struct UnitWalk {
   }
 };
 
-// The unit that is cut at the start of CTA c's run, if that is its first cut:
-// its shares lie with the CTAs c - 1 .. last. Share k is slot(k): a CTA has
-// two slots, one for its first segment and one for a later one.
+// The unit that is cut at the start of CTA c's run: its n shares lie with
+// consecutive CTAs, share k at slot(k) (a CTA has two slots, one for its first
+// segment and one for a later one), and c is the nth-th of its n - 1 cuts. All
+// lanes of a warp call find, which reads the starts of 32 CTAs to either side
+// at once.
 struct Cut {
   Start st;
-  int c, last, slot0;
-  __device__ bool find(const Plan* plan, int c_) {
-    c = c_;
-    if (c >= plan->ctas) return false;
-    st = plan->start[c];
-    const Start before = plan->start[c - 1];
-    const bool same = before.k == st.k && before.hk == st.hk && before.unit == st.unit;
-    if (st.t0 == 0 || (same && before.t0 > 0)) return false;
-    slot0 = 2 * (c - 1) + (same ? 0 : 1);
-    last = c;
-    while (last + 1 < plan->ctas) {
-      const Start a = plan->start[last + 1];
-      if (a.k != st.k || a.hk != st.hk || a.unit != st.unit) break;
-      ++last;
+  Seq s;
+  int b, n, nth, slot0, slot1;
+  __device__ bool find(const Plan* plan, int c) {
+    const int lane = lane_id();
+    auto start = [&](int i) { return i >= 0 && i < kMaxRuns ? plan->begin[i].st : Start{-1, -1, -1, -1}; };
+    Start back = start(c - 1 - lane), on = start(c + 1 + lane);
+    const Begin mine = plan->begin[c];
+    const int ctas = plan->ctas;
+    if (c >= ctas || mine.st.t0 == 0) return false;
+    st = mine.st;
+    s = mine.s;
+    b = mine.b;
+    auto within = [&](const Start& x) { return x.k == st.k && x.hk == st.hk && x.unit == st.unit; };
+    int first = c, last = c;  // of the CTAs that start in the unit, past its beginning
+    bool same;                // the CTA before those starts at its beginning
+    for (;;) {
+      const bool in = within(back);
+      const uint32_t m = __ballot_sync(0xffffffffu, in && back.t0 > 0);
+      const int t = m == 0xffffffffu ? 32 : __ffs(~m) - 1;
+      first -= t;
+      if (t < 32) {
+        same = __shfl_sync(0xffffffffu, in, t);
+        break;
+      }
+      back = start(first - 1 - lane);
     }
+    for (;;) {
+      const uint32_t m = __ballot_sync(0xffffffffu, last + 1 + lane < ctas && within(on));
+      const int t = m == 0xffffffffu ? 32 : __ffs(~m) - 1;
+      last += t;
+      if (t < 32) break;
+      on = start(last + 1 + lane);
+    }
+    n = last - first + 2;
+    nth = c - first;
+    slot0 = 2 * (first - 1) + (same ? 0 : 1);
+    slot1 = 2 * first;
     return true;
   }
-  __device__ int slot(int k) const { return k < c ? slot0 : 2 * k; }
+  __device__ int slot(int k) const { return k == 0 ? slot0 : slot1 + 2 * (k - 1); }
 };
 
 }  // namespace paged

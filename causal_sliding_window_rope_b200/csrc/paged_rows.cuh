@@ -5,7 +5,7 @@
 // with its join: 32 sequences of 2048 rows, 12 heads on 4 of 128, 28.0 us =
 // 4.8 TB/s (0.73 of a copy's rate), about 3 us of it the CTAs' start (lengths,
 // page table, first copy: dependent loads) and 3 the launches; one sequence of
-// 1000 rows, 6 heads, 9.8 us.
+// 1000 rows, 6 heads, 9.1 us.
 //
 // Work is cut by bytes, not by sequence: the 64-row blocks of all (sequence,
 // KV head) pairs in a row are dealt out evenly to one CTA per SM, so ragged

@@ -24,8 +24,10 @@
 // while the last one's output is still being written.
 // Bound by the chain of a tile (S, softmax, P V, next S: about 3200 cycles a
 // block, the products 2050 of them) and, in long runs, by the power limit
-// (1.6 GHz): 2 x 2048 tokens of 16 heads on 4 over 8192 rows 253 us = 951
-// TFLOP/s (0.58 of the burst, 0.68 of the sustained rate of a matrix product).
+// (1.6 GHz): 2 x 2048 tokens of 16 heads on 4 over 8192 rows 245 us = 980
+// TFLOP/s (0.60 of the burst, 0.70 of the sustained rate of a matrix product).
+// Short chunks are bound by latency: lengths, page table, first copy and first
+// block, 18 thousand cycles of the 33 of a CTA with four blocks.
 // Two warps that issue, one per tile, let the tiles fall into step: 302 us.
 #pragma once
 #include "paged_rows.cuh"
@@ -144,7 +146,24 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       uint8_t* my_dst = smem + SM::kOffKV + my_panel * SM::kPanel + my_unit * p.unit * 128;
       int slot = 0, use = 0, issued = 0, segs = 0, q_issued = 0;
       bool ok = true;
+      auto load_q = [&](const TileWalk& w) {
+        if (lane == 0) {
+          const uint32_t bytes = p.tpt * v.g * 128 * NP;
+          mbar_expect_tx(q_full, w.tokens(1) ? 2 * bytes : bytes);
+          for (int X = 0; X < 2; ++X) {
+            if (!w.tokens(X)) continue;
+            for (int pn = 0; pn < NP; ++pn)
+              tma_load_3d(&tmQ, q_full, smem + X * SM::kOp + pn * SM::kPanel, 64 * pn, w.hk * v.g,
+                          w.s.tok0 + (2 * w.u + X) * p.tpt);
+          }
+        }
+        ++q_issued;
+        __syncwarp();
+      };
       for (TileWalk w(p, run); ok && w.valid(); w.next(), ++segs) {
+        // The first Q tiles go out before the page table is read, later ones
+        // behind their unit's first block: their buffer frees last.
+        if (segs == 0) load_q(w);
         UnitPages up(v, w.seq(), w.s, w.first * 128 + my_unit * p.unit, 128, p.unit);
         for (int t = w.t0; ok && t < w.t1; ++t) {
           const int page = up.page(t, lane < boxes), row_slot = up.slot(t);
@@ -163,21 +182,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
               ++use;
             }
           }
-          if (ok && t == w.t0) {  // the Q tiles, behind the first block: their buffer frees last
-            if (segs > 0) ok = __all_sync(0xffffffffu, mbar_wait(q_empty, (segs - 1) & 1, wc));
+          if (ok && segs > 0 && t == w.t0) {
+            ok = __all_sync(0xffffffffu, mbar_wait(q_empty, (segs - 1) & 1, wc));
             if (!ok) break;
-            if (lane == 0) {
-              const uint32_t bytes = p.tpt * v.g * 128 * NP;
-              mbar_expect_tx(q_full, w.tokens(1) ? 2 * bytes : bytes);
-              for (int X = 0; X < 2; ++X) {
-                if (!w.tokens(X)) continue;
-                for (int pn = 0; pn < NP; ++pn)
-                  tma_load_3d(&tmQ, q_full, smem + X * SM::kOp + pn * SM::kPanel, 64 * pn, w.hk * v.g,
-                              w.s.tok0 + (2 * w.u + X) * p.tpt);
-              }
-            }
-            ++q_issued;
-            __syncwarp();
+            load_q(w);
           }
         }
         if (!ok) break;
@@ -462,84 +470,133 @@ struct JoinParams {
   const float2* part_ml;
   const int2* info;  // of rows_kernel
   const Plan* plan;  // of tile_kernel
-  const int* seqs;
   __nv_bfloat16* O;
   float* lse;
 };
 
-constexpr int kJoinWarps = 8;  // output rows of a CTA
+constexpr int kJoinWarps = 8;
+constexpr int kJoinRows = 4;                                   // rows of a warp where units of few shares are joined
+constexpr int kJoinFew = 8;                                    // shares
+constexpr int kJoinUnitCtas = 256 / (kJoinWarps * kJoinRows);  // CTAs of a unit's cut
 
-// One output row by one warp, from n partials (maximum, sum, output):
-// O = sum 2^(m - M) O_i / sum 2^(m - M) l_i; at(i) is the place of the i-th.
-template <int D, class At>
-__device__ __forceinline__ void join_row(const float* part_o, const float2* part_ml, int n, const At& at,
-                                         __nv_bfloat16* O, float* lse) {
-  const int lane = lane_id();
+// R output rows by one warp, rows row0 .. of n partials (maximum, sum,
+// output): O = sum 2^(m - M) O_i / sum 2^(m - M) l_i; at(i) is the i-th one's
+// place, live a bit per row, to(j) the j-th row's place in O and lse. 32 / R
+// lanes have a row's maxima and sums, all of them its output, of which R E
+// loads are in flight.
+template <int D, int R, int E, class At, class To>
+__device__ __forceinline__ void join_rows(const float* part_o, const float2* part_ml, int n, const At& at, int row0,
+                                          uint32_t live, const To& to, __nv_bfloat16* O, float* lse) {
+  constexpr int W = 32 / R, C = D / 32;
+  const int lane = lane_id(), mine = lane / W, k_mine = lane % W;
+  const bool on = (live >> mine) & 1u;
   float M = -INFINITY;
-  for (int k = lane; k < n; k += 32) M = fmaxf(M, part_ml[at(k)].x);
+  for (int k = k_mine; k < n; k += W)
+    if (on) M = fmaxf(M, part_ml[at(k) + row0 + mine].x);
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float L = 0.f, a[D / 32];
+  for (int o = W / 2; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float L = 0.f, a[R][C];
 #pragma unroll
-  for (int e = 0; e < D / 32; ++e) a[e] = 0.f;
-#pragma unroll 4
-  for (int k = 0; k < n; ++k) {
-    const float2 x = part_ml[at(k)];
-    if (x.x == -INFINITY) continue;  // no key of this share: its output may not be written
-    const float f = ex2(x.x - M);
+  for (int j = 0; j < R; ++j)
+#pragma unroll
+    for (int e = 0; e < C; ++e) a[j][e] = 0.f;
+  for (int k0 = 0; k0 < n; k0 += W) {
+    const float2 x = on && k0 + k_mine < n ? part_ml[at(k0 + k_mine) + row0 + mine] : make_float2(-INFINITY, 0.f);
+    const float f = x.x == -INFINITY ? 0.f : ex2(x.x - M);  // 0: no key of this share, its output may not be written
     L = fmaf(x.y, f, L);
-    const float* src = part_o + at(k) * D + lane * (D / 32);
+    const int m = min(W, n - k0);
+#pragma unroll 1
+    for (int kk = 0; kk < m; kk += E) {
+      float y[E][R][C], g[E][R];
 #pragma unroll
-    for (int e = 0; e < D / 32; e += 2) {
-      const float2 y = *reinterpret_cast<const float2*>(src + e);
-      a[e] = fmaf(y.x, f, a[e]);
-      a[e + 1] = fmaf(y.y, f, a[e + 1]);
+      for (int i = 0; i < E; ++i) {
+        const float* src = part_o + (at(k0 + kk + i) + row0) * D + lane * C;
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+          g[i][j] = __shfl_sync(0xffffffffu, f, j * W + kk + i);  // 0 past the last share
+#pragma unroll
+          for (int e = 0; e < C; ++e) y[i][j][e] = 0.f;
+          if (g[i][j] != 0.f) {
+            if constexpr (C == 4) {
+              const float4 t = *reinterpret_cast<const float4*>(src + j * D);
+              y[i][j][0] = t.x, y[i][j][1] = t.y, y[i][j][2] = t.z, y[i][j][3] = t.w;
+            } else {
+              const float2 t = *reinterpret_cast<const float2*>(src + j * D);
+              y[i][j][0] = t.x, y[i][j][1] = t.y;
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < E; ++i)
+#pragma unroll
+        for (int j = 0; j < R; ++j)
+#pragma unroll
+          for (int e = 0; e < C; ++e) a[j][e] = fmaf(y[i][j][e], g[i][j], a[j][e]);
     }
   }
-  const float inv = 1.f / L;
 #pragma unroll
-  for (int e = 0; e < D / 32; e += 2)
-    *reinterpret_cast<uint32_t*>(O + lane * (D / 32) + e) = pack_bf16x2(a[e] * inv, a[e + 1] * inv);
-  if (lane == 0) *lse = (M + log2f(L)) * 0.69314718055994531f;
+  for (int o = W / 2; o >= 1; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+#pragma unroll
+  for (int j = 0; j < R; ++j) {
+    const float inv = 1.f / __shfl_sync(0xffffffffu, L, j * W);
+    if (!((live >> j) & 1u)) continue;
+    __nv_bfloat16* dst = O + to(j) * D + lane * C;
+#pragma unroll
+    for (int e = 0; e < C; e += 2)
+      *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(a[j][e] * inv, a[j][e + 1] * inv);
+  }
+  if (on && k_mine == 0) lse[to(mine)] = (M + log2f(L)) * 0.69314718055994531f;
 }
 
 // CTA = a (sequence, KV head) pair, joined if rows_kernel cut it; or, with
-// TILES, a boundary between two CTAs' runs of tile_kernel and 8 of the 256
-// rows of the unit cut there.
+// TILES, a cut between two CTAs' runs of tile_kernel and rows of the unit that
+// lies there: 32 of its 256, by the CTAs of its first cut, or, of a unit in
+// more than kJoinFew shares, 8 by those of each of its first kJoinRows cuts (a
+// chunk of 64 tokens over 20000 rows, 37 shares: 36 us, 70 with the former).
 template <int D, bool TILES>
-__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const JoinParams p) {
+__global__ void __launch_bounds__(32 * kJoinWarps, TILES ? 4 : 1) join_kernel(const JoinParams p) {
   pdl_launch_dependents();
   pdl_wait();
   const View& v = p.v;
-  Seq s{};
-  auto out_row = [&](int hk, int i, int h) { return static_cast<size_t>(s.tok0 + i) * v.H + hk * v.g + h; };
   if constexpr (!TILES) {
     const int b = blockIdx.x / v.Hk, hk = blockIdx.x % v.Hk;
     // Unspecified for a sequence without tokens, and where a wait of
     // rows_kernel has run out: what does not name slots is not followed.
     const int2 inf = p.info[blockIdx.x];
     int first;
+    Seq s;
     seq_load(v, b, false, s);
     if (visible_blocks(v, s, p.rows, first) == 0 || inf.y <= 1) return;
     if (inf.x < 0 || inf.x >= 2 * kSMs || inf.y > kSMs - (inf.x >> 1)) return;
-    for (int r = warp_id(); r < s.n * v.g; r += kJoinWarps) {
-      const size_t row = out_row(hk, r / v.g, r % v.g);
-      join_row<D>(p.part_o, p.part_ml, inf.y,
-                  [&](int k) { return static_cast<size_t>(k == 0 ? inf.x : 2 * ((inf.x >> 1) + k)) * p.rows + r; },
-                  p.O + row * D, p.lse + row);
-    }
+    for (int r = warp_id(); r < s.n * v.g; r += kJoinWarps)
+      join_rows<D, 1, 8>(
+          p.part_o, p.part_ml, inf.y,
+          [&](int k) { return static_cast<size_t>(k == 0 ? inf.x : 2 * ((inf.x >> 1) + k)) * p.rows; }, r, 1u,
+          [&](int) { return static_cast<size_t>(s.tok0 + r / v.g) * v.H + hk * v.g + r % v.g; }, p.O, p.lse);
   } else {
-    const int x = blockIdx.x;
     Cut cut;
-    if (!cut.find(p.plan, x / (256 / kJoinWarps) + 1)) return;
-    seq_load(v, p.seqs[cut.st.k], false, s);
-    const int row = x % (256 / kJoinWarps) * kJoinWarps + warp_id();  // of the unit's two tiles
-    const int r = row & 127, i = (2 * cut.st.unit + (row >> 7)) * p.tpt + r / v.g;
-    if (r >= p.tpt * v.g || i >= s.n) return;
-    const size_t o = out_row(cut.st.hk, i, r % v.g);
-    join_row<D>(p.part_o, p.part_ml, cut.last - cut.c + 2,
-                [&](int k) { return static_cast<size_t>(cut.slot(cut.c - 1 + k)) * 256 + row; }, p.O + o * D,
-                p.lse + o);
+    if (!cut.find(p.plan, blockIdx.x / kJoinUnitCtas + 1)) return;
+    const bool many = cut.n > kJoinFew;
+    if (cut.nth >= (many ? kJoinRows : 1)) return;
+    const int w = blockIdx.x % kJoinUnitCtas * kJoinWarps + warp_id();
+    // Rows of the unit's two tiles.
+    const int row0 = many ? kJoinRows * w + cut.nth : kJoinRows * w, rows = many ? 1 : kJoinRows;
+    const int r0 = row0 & 127, i0 = (2 * cut.st.unit + (row0 >> 7)) * p.tpt;
+    uint32_t live = 0u;
+#pragma unroll
+    for (int j = 0; j < kJoinRows; ++j)
+      if (j < rows && r0 + j < p.tpt * v.g && i0 + (r0 + j) / v.g < cut.s.n) live |= 1u << j;
+    if (live == 0u) return;
+    auto at = [&](int k) { return static_cast<size_t>(cut.slot(k)) * 256; };
+    auto to = [&](int j) {
+      return static_cast<size_t>(cut.s.tok0 + i0 + (r0 + j) / v.g) * v.H + cut.st.hk * v.g + (r0 + j) % v.g;
+    };
+    // As many loads as 64 registers hold: four CTAs on an SM are worth more
+    // (2 x 2048 tokens over 8192 rows 245 us, 250 with twice the loads).
+    constexpr int kLoads = D == 128 ? 4 : 8;
+    if (many) join_rows<D, 1, kLoads>(p.part_o, p.part_ml, cut.n, at, row0, live, to, p.O, p.lse);
+    else join_rows<D, kJoinRows, kLoads / kJoinRows>(p.part_o, p.part_ml, cut.n, at, row0, live, to, p.O, p.lse);
   }
 }
 

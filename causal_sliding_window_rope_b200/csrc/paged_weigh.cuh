@@ -17,7 +17,7 @@
 //   weigh_tile_kernel   many: tcgen05, 128 cached rows x 128 query rows per
 //     product, two threads per cached row; bound by the exponentials (one per
 //     score on the MUFU unit, 57 % busy). 2213 tokens of 16 heads on 4 over
-//     11081 rows 65 us = 520 TFLOP/s.A call with a chunk runs it for its
+//     11081 rows 64 us = 530 TFLOP/s.A call with a chunk runs it for its
 //     single tokens too.
 #pragma once
 #include "paged_tile.cuh"
@@ -503,17 +503,16 @@ __global__ void __launch_bounds__(128) weigh_join_kernel(const __grid_constant__
   pdl_launch_dependents();
   pdl_wait();
   Cut cut;
-  if (!cut.find(p.plan, blockIdx.x + 1)) return;
+  if (!cut.find(p.plan, blockIdx.x + 1) || cut.nth != 0) return;
   const View& v = p.v;
-  const int b = p.seqs[cut.st.k];
-  Seq s;
-  seq_load(v, b, false, s);
+  const Seq& s = cut.s;
   const int key = RowUnits{p.tpt}.first_row(v, s, cut.st.unit) + threadIdx.x;
   if (key >= s.L + s.n || key <= s.L - v.W) return;
-  const int page = page_at(v, b, page_entry(v, key));
+  const int page = page_at(v, cut.b, page_entry(v, key));
   if (page < 0) return;
   float total = 0.f;
-  for (int k = cut.c - 1; k <= cut.last; ++k) total += p.part[static_cast<size_t>(cut.slot(k)) * 128 + threadIdx.x];
+#pragma unroll 4
+  for (int k = 0; k < cut.n; ++k) total += p.part[static_cast<size_t>(cut.slot(k)) * 128 + threadIdx.x];
   p.weight[term_index(v, page, page_slot(v, key), cut.st.hk)] += total;
 }
 

@@ -170,6 +170,20 @@ def test_weigh(lens, news, H, Hk, D, page, W, cap, pad):
     assert torch.equal(again.weight, cache.weight)
 
 
+@pytest.mark.parametrize("lens,news,H,Hk,D", [
+    ([12000], [40], 4, 1, 128),    # a unit of 160 rows over 94 blocks: 47 shares
+    ([9000, 0], [9, 3], 8, 1, 64),
+    ([5000], [30], 8, 4, 128),     # 20 shares a head
+    ([12000], [2], 12, 4, 128),    # few rows: pairs cut in 37
+    ([16000], [1], 6, 1, 64),      # ... one in 125
+    ([0], [100], 128, 1, 64),      # one tile of cached rows under 100 tiles of query rows
+    ([28], [100], 128, 1, 128),
+])
+def test_work_cut_in_many_shares(lens, news, H, Hk, D):
+    test_attend(lens, news, H, Hk, D, 64, None, None, 1)
+    test_weigh(lens, news, H, Hk, D, 64, None, None, 1)
+
+
 @pytest.mark.parametrize("news", [[1, 1], [40, 1], [1, 300]])
 def test_other_scale_and_large_scores(news):
     """Scores up to hundreds: only the largest key counts, nothing overflows."""
