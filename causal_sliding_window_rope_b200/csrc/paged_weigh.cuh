@@ -13,7 +13,7 @@
 //   weigh_rows_kernel   few (<= 32): bound by reading K once and by the start
 //     of a CTA. Blocks of 64 cached rows, dealt out evenly as in the attention
 //     of few rows; mma.sync with K as the first operand, the query rows as
-//     columns (8 per product). 32 ragged sequences of up to 2048 rows 12.8 us.
+//     columns (8 per product). 32 ragged sequences of up to 2048 rows 12.7 us.
 //   weigh_tile_kernel   many: tcgen05, 128 cached rows x 128 query rows per
 //     product, two threads per cached row; bound by the exponentials (one per
 //     score on the MUFU unit, 57 % busy). 2213 tokens of 16 heads on 4 over
