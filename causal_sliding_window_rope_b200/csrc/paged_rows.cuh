@@ -32,7 +32,9 @@ namespace paged {
 
 constexpr int kBlk = 64;         // cached rows of a block
 constexpr int kKeyGroups = 4;    // warps that share a block, 16 rows each
-constexpr int kMinBlocks = 2;    // fewest blocks worth a CTA of their own (one chat over 1000 rows: 1 10.8 us, 2 9.8, 4 10.6)
+// Fewest blocks worth a CTA of their own (one chat over 1000 rows: 1 9.0 us, 2
+// 9.1, 4 10.5; 2 leaves half the shares to join).
+constexpr int kMinBlocks = 2;
 
 struct RowsParams {
   View v;
