@@ -43,7 +43,7 @@ template <int D>
 struct WeighRowsSmem {
   static constexpr int kPanel = kBlk * 128;
   static constexpr int kStage = (D / 64) * kPanel;   // a block of K
-  static constexpr int kStages = D == 128 ? 10 : 16;
+  static constexpr int kStages = D == 128 ? 12 : 16;
   static constexpr int kOffBar = kStages * kStage;
   static constexpr int kOffPre = kOffBar + 8 * (2 * kStages + 2);
   static constexpr int kBytes = kOffPre + 1024;      // and 4 (B + 1) more
@@ -63,6 +63,10 @@ __global__ void __launch_bounds__(32 * (4 * WeighGroups<NT>::value + 1), 1)
     weigh_rows_kernel(const __grid_constant__ CUtensorMap tmK, const WeighRowsParams p) {
   using SM = WeighRowsSmem<D>;
   constexpr int NS = SM::kStages, NP = D / 64, kGroups = WeighGroups<NT>::value, kWarps = 4 * kGroups;
+  // A wait for a slot's phase parity returns too while the phase before it is
+  // still open. A group waits for its own blocks only, so a slot's uses must
+  // all be one group's: that of its next block has then seen its last one land.
+  static_assert(NS % kGroups == 0, "a slot's blocks belong to one group of warps");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_align1024(smem_raw);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::kOffBar);
