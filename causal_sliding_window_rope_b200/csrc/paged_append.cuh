@@ -59,11 +59,12 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
   pdl_wait();
   for (int b = threadIdx.x; b < v.B; b += kAppendThreads) {
     const int lo = v.new_start[b], hi = v.new_start[b + 1];
-    if (blockIdx.x == 0) {  // one CTA reports lengths that do not fit
-      Seq s;
-      seq_load(v, b, true, s);
-    }
-    for (int tt = max(0, lo - t0); tt < min(ntt, hi - t0); ++tt) s_seq[tt] = b;
+    // Only a sequence whose lengths fit has tokens: the range of one that does
+    // not may lie over another's. One CTA reports them.
+    const bool here = lo < t0 + ntt && hi > t0;
+    Seq s;
+    if (!(here || blockIdx.x == 0) || !seq_load(v, b, blockIdx.x == 0, s)) continue;
+    for (int tt = max(0, s.tok0 - t0); tt < min(ntt, s.tok0 + s.n - t0); ++tt) s_seq[tt] = b;
   }
   __syncthreads();
   if (threadIdx.x < ntt) {
@@ -71,12 +72,11 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
     int page = -1;
     if (b >= 0) {
       Seq s;
-      if (seq_load(v, b, false, s)) {
-        const int row = s.L + (t0 + tt - s.tok0);
-        page = page_at(v, b, page_entry(v, row));
-        s_slot[tt] = page_slot(v, row);
-        s_pos[tt] = p.positions ? p.positions[t0 + tt] : row;
-      }
+      seq_load(v, b, false, s);
+      const int row = s.L + (t0 + tt - s.tok0);
+      page = page_at(v, b, page_entry(v, row));
+      s_slot[tt] = page_slot(v, row);
+      s_pos[tt] = p.positions ? p.positions[t0 + tt] : row;
     }
     s_page[tt] = page;  // -1: the token belongs to nobody, or has no place
   }

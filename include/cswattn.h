@@ -324,7 +324,8 @@ cswattn_status attn_decode(const cswattn_layer* layer, const void* q, const void
  * n_tokens or max_new, rows past T) is left untouched, and so is a token or row
  * whose page is not in [0, n_pages); the next cswattn_sync_status() returns
  * CSWATTN_ERR_INVALID_ARG. (The attention of a sequence with such a page is
- * computed as if its rows were zeros.) */
+ * computed as if its rows were zeros. Where new_start decreases, two sequences
+ * that fit may claim the same tokens: those are either's.) */
 typedef struct {
   int page_size;         /* rows of a page, a multiple of 16 */
   int n_pages;           /* pages of the pools */
