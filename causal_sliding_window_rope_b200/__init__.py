@@ -338,7 +338,8 @@ def _rope(R, interleaved, scaling, factor, base, original_length, beta_fast, bet
             def pair_of(turns):  # the pair that turns this often within original_length
                 return R * math.log(original_length / (turns * 2 * math.pi)) / (2 * math.log(base))
             low = max(math.floor(pair_of(beta_fast)), 0)
-            high = min(math.ceil(pair_of(beta_slow)), R // 2 - 1)
+            # (the line may end past the last pair, R / 2 - 1, which then keeps a part of its frequency)
+            high = min(math.ceil(pair_of(beta_slow)), R - 1)
             for i in range(R // 2):
                 ramp = min(max((i - low) / max(high - low, 0.001), 0.0), 1.0)
                 w[i] = w[i] * (1 - ramp) + w[i] / factor * ramp
