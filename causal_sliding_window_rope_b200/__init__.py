@@ -343,7 +343,7 @@ def _rope(R, interleaved, scaling, factor, base, original_length, beta_fast, bet
             for i in range(R // 2):
                 ramp = min(max((i - low) / max(high - low, 0.001), 0.0), 1.0)
                 w[i] = w[i] * (1 - ramp) + w[i] / factor * ramp
-            scale = 0.1 * math.log(factor) + 1.0
+            scale = 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0
     scale = float(scale if attention_factor is None else attention_factor)
     struct = CswattnRope(R, int(interleaved), scale, (ctypes.c_double * len(w))(*w))
     return tuple(w), scale, struct, ctypes.addressof(struct)
@@ -360,7 +360,7 @@ class RopeSpec:
     "yarn"     pairs that turn more than ``beta_fast`` times within
                ``original_length`` positions as they are, those below
                ``beta_slow`` turns divided by ``factor``, a ramp between, and
-               cos and sin times 0.1 ln(factor) + 1
+               cos and sin times 0.1 ln(factor) + 1 (1 for a factor below 1)
 
     or ``frequencies``: one angle per position for each pair, in their place.
     ``attention_factor`` replaces the factor on cos and sin.

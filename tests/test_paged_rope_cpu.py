@@ -22,3 +22,8 @@ def test_ramped_frequencies(R, base, original, factor):
         turns = original * w / (2 * math.pi)
         if turns > 1.0:
             assert f > w / factor * (1 + 1e-9), (i, turns)
+
+
+@pytest.mark.parametrize("factor,want", [(0.25, 1.0), (1.0, 1.0), (4.0, 1 + 0.1 * math.log(4.0))])
+def test_a_context_that_is_not_stretched_keeps_cos_and_sin(factor, want):
+    assert cs.RopeSpec(64, scaling="yarn", factor=factor, original_length=2048).attention_factor == pytest.approx(want)
