@@ -363,19 +363,38 @@ class RopeSpec:
                cos and sin times 0.1 ln(factor) + 1 (1 for a factor below 1)
 
     or ``frequencies``: one angle per position for each pair, in their place.
-    ``attention_factor`` replaces the factor on cos and sin.
+    ``attention_factor`` replaces the factor on cos and sin. ``base`` None is
+    the ``rope_base`` of the layer that a call is made with (``of``); until
+    then ``frequencies`` are those of the usual 10000.
     """
 
     SCALINGS = ("none", "linear", "ntk", "yarn")
 
-    def __init__(self, rotary_dim, interleaved=False, scaling="none", factor=1.0, base=10000.0,
+    DEFAULT_BASE = 10000.0
+
+    def __init__(self, rotary_dim, interleaved=False, scaling="none", factor=1.0, base=None,
                  original_length=None, beta_fast=32.0, beta_slow=1.0, attention_factor=None, frequencies=None):
         self.rotary_dim, self.interleaved = int(rotary_dim), bool(interleaved)
         if frequencies is not None:
             frequencies = tuple(float(f) for f in frequencies)
+        # the layer's base still to come: how to make this of another one
+        self._open = None
+        if base is None:
+            base = self.DEFAULT_BASE
+            if frequencies is None:
+                self._open = (self.rotary_dim, self.interleaved, scaling, factor, original_length, beta_fast, beta_slow,
+                              attention_factor)
         self.frequencies, self.attention_factor, self._c, self.address = _rope(
             self.rotary_dim, self.interleaved, scaling, factor, base, original_length, beta_fast, beta_slow,
             attention_factor, frequencies)
+
+    def of(self, spec: LayerSpec) -> RopeSpec:
+        """This rotation in a layer: with the layer's base where none was given."""
+        if self._open is None or spec.rope_base == self.DEFAULT_BASE:
+            return self
+        R, interleaved, scaling, factor, *rest = self._open
+        # the float32 that the layer's C struct holds
+        return RopeSpec(R, interleaved, scaling, factor, ctypes.c_float(spec.rope_base).value, *rest)
 
 
 _paged = None
@@ -442,6 +461,8 @@ def attn_paged_append(spec: LayerSpec, batch: PagedBatch, cache: PagedCache, q, 
                       positions=None, rope: RopeSpec | None = None, stream=None):
     """The prologue of the batch's new tokens: q_out, and their rows of the
     cache. rope None: the layer's plain RoPE."""
+    if rope is not None:
+        rope = rope.of(spec)
     (_paged or _paged_calls()).append(spec, batch, cache, q, k, v, ve, gate, q_out, positions, rope, stream)
 
 

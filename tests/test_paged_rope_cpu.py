@@ -27,3 +27,30 @@ def test_ramped_frequencies(R, base, original, factor):
 @pytest.mark.parametrize("factor,want", [(0.25, 1.0), (1.0, 1.0), (4.0, 1 + 0.1 * math.log(4.0))])
 def test_a_context_that_is_not_stretched_keeps_cos_and_sin(factor, want):
     assert cs.RopeSpec(64, scaling="yarn", factor=factor, original_length=2048).attention_factor == pytest.approx(want)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(), 5e5), (dict(base=2e4), 2e4), (dict(base=10000.0), 1e4),
+    (dict(scaling="linear", factor=4.0), 5e5), (dict(scaling="ntk", factor=2.0), 5e5),
+    (dict(scaling="yarn", factor=4.0, original_length=8192), 5e5),
+])
+def test_the_layers_base_is_the_default(kw, want, monkeypatch):
+    """What attn_paged_append hands to the library: frequencies of the layer's base unless the RopeSpec names one."""
+    seen = []
+
+    class Calls:
+        @staticmethod
+        def append(*a):
+            s = cs.CswattnRope.from_address(a[10].address)
+            seen.append([s.frequencies[i] for i in range(s.rotary_dim // 2)])
+    monkeypatch.setattr(cs, "_paged", Calls)
+    rope = cs.RopeSpec(64, **kw)
+    for base in (5e5, 1e4, 5e5):
+        spec = cs.LayerSpec(1, 16, 2, 1, 64, 16, has_ve=False, rope_base=base)
+        cs.attn_paged_append(spec, *[None] * 8, rope=rope)
+        explicit = cs.RopeSpec(64, **{**kw, "base": want if want != 5e5 else base})
+        assert seen[-1] == list(explicit.frequencies)
+    assert seen[0] == seen[2] and (seen[0] != seen[1]) == (want == 5e5)
+    own = cs.RopeSpec(16, frequencies=[0.5] * 8)
+    cs.attn_paged_append(cs.LayerSpec(1, 16, 2, 1, 64, 16, has_ve=False, rope_base=5e5), *[None] * 8, rope=own)
+    assert seen[-1] == [0.5] * 8
