@@ -443,8 +443,12 @@ class PagedCache:
 class PagedBatch:
     """The sequences of a paged call: page_table (B, pages_per_seq), cache_len
     (B) and new_start (B + 1), int32 device tensors; n_tokens rows of q, and
-    the most new tokens a sequence has (new_start, n_tokens and max_new are
-    not needed to select and move rows)."""
+    max_new, which no sequence's new tokens exceed (new_start, n_tokens and
+    max_new are not needed to select and move rows). max_new chooses the
+    kernels, by max_new times the heads of a group: above 32 those of long
+    chunks run, for single tokens too. A tight bound is the fast one:
+    called alone, a step of 32 sequences of 2048 rows, 12 heads on 4 of 128,
+    takes 39 us with max_new 1 and 49 us with 512, its row weights 18 and 28."""
 
     def __init__(self, page_table, cache_len, new_start=None, n_tokens=0, max_new=0):
         (_paged or _paged_calls()).check_batch(page_table, cache_len, new_start)

@@ -1,6 +1,10 @@
 """The paged cache as a serving program meets it: batches that hold a sequence
 which does not fit, the documented loop, captured loops, what is left after an
 eviction."""
+import os
+import re
+import types
+
 import pytest
 import torch
 
@@ -52,3 +56,36 @@ def test_tokens_of_a_sequence_beside_one_that_does_not_fit(start, max_new):
     for alone, beside in zip(*outs):
         assert torch.equal(alone.view(torch.int16 if alone.dtype == BF else torch.int32),
                            beside.view(torch.int16 if beside.dtype == BF else torch.int32))
+
+
+def test_the_documented_loop():
+    """README's serving loop, word for word: prompts' chunks beside single tokens, then generation until rows go."""
+    readme = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")).read()
+    code = re.search(r"A serving loop over a paged cache.*?```python\n(.*?)```", readme, re.S).group(1)
+    g = torch.Generator(device="cuda").manual_seed(71)
+    B, H, Hk, D, K = 32, 16, 4, 128, 4096
+    length, next_pos = torch.zeros(B, **I32), torch.zeros(B, **I32)
+    page_table = torch.randperm(4096, generator=g, device="cuda").to(torch.int32).view(B, 128)
+    total = [0] * B
+    for news in ([2500, 1, 7] + [0] * 29, [2500] + [60] * 31, [1] * B, [0, 1] * 16):
+        start = torch.tensor([sum(news[:b]) for b in range(B + 1)], **I32)
+        N, most = sum(news), max(news)
+        r = lambda h: torch.randn(N, h, D, generator=g, device="cuda").to(BF)  # noqa: E731
+        q, k, v = r(H), r(Hk), r(Hk)
+        token = torch.arange(N, device="cuda")
+        b = torch.searchsorted(start[1:].long(), token, right=True)
+        positions = (next_pos[b] + token - start[b]).to(torch.int32)
+        next_pos += start[1:] - start[:-1]
+        q_out, O = torch.empty_like(q), torch.full_like(q, float("nan"))
+        lse = torch.full((N, H), float("nan"), device="cuda")
+        n_moves, new_len = torch.empty(B, Hk, **I32), torch.empty(B, **I32)
+        src, dst = torch.empty(B, Hk, K, **I32), torch.empty(B, Hk, K, **I32)
+        space = dict(locals(), torch=torch, cs=cs)
+        if total[0]:
+            space["cs"] = types.SimpleNamespace(**{**vars(cs), "PagedCache": lambda *a, **kw: cache})  # the one there is
+        exec(code, space)
+        cache = space["cache"]
+        cs.cswattn_sync_status()
+        total = [min(K, t + n) for t, n in zip(total, news)]
+        assert length.tolist() == total and torch.isfinite(O.float()).all() and torch.isfinite(lse).all()
+        assert (n_moves[1:] == 0).all() and bool((n_moves[0] > 0).all()) == (news[0] > 0 and total[0] == K)
