@@ -99,7 +99,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(q_full + 10);
   const View& v = p.v;
   const int warp = warp_id(), lane = lane_id(), c = blockIdx.x;
-  pdl_launch_dependents();
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
       mbar_init(&kv_full[s], 1);
@@ -129,6 +128,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // Not before: a successor that takes tensor memory ahead of its wait for this
+  // kernel, beside a CTA that has not taken its own yet, would block it.
+  pdl_launch_dependents();
   const uint32_t tmem = *tmem_slot;
   const WaitCtx wc{abort_flag, p.wait_ns};
 

@@ -276,7 +276,6 @@ __global__ void __launch_bounds__(kWeighThreads, 2)
   uint64_t* t_full = k_full + 17;    // [kTerms] -lse log2(e) of a tile's query rows written (32 arrivals)
   const View& v = p.v;
   const int warp = warp_id(), lane = lane_id(), c = blockIdx.x;
-  pdl_launch_dependents();
   if (threadIdx.x == 0) {
     mbar_init(k_full, 1);
     mbar_init(k_empty, 1);
@@ -306,6 +305,9 @@ __global__ void __launch_bounds__(kWeighThreads, 2)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // Not before: a successor that takes tensor memory ahead of its wait for this
+  // kernel, beside a CTA that has not taken its own yet, would block it.
+  pdl_launch_dependents();
   const uint32_t tmem = *tmem_slot;
   const WaitCtx wc{abort_flag, p.wait_ns};
   UnitWalk<RowUnits> w(v, RowUnits{p.tpt}, run, p.seqs);
