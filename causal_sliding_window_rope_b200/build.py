@@ -9,9 +9,11 @@ a machine that has no GPU driver.
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -58,15 +60,36 @@ def binding_deps() -> list[str]:
     return [BINDING_SOURCE, HEADER, os.path.abspath(__file__)]
 
 
+def torch_dir() -> str | None:
+    """Where PyTorch is installed, without importing it."""
+    try:
+        spec = importlib.util.find_spec("torch")
+    except ValueError:
+        return None
+    return os.path.dirname(spec.origin) if spec and spec.origin else None
+
+
+def binding_lacks() -> str | None:
+    """What this machine lacks to compile the Python module, or None."""
+    base = torch_dir()
+    if base is None:
+        return "PyTorch"
+    if not os.path.exists(os.path.join(base, "include", "torch", "csrc", "autograd", "python_variable.h")):
+        return "PyTorch's headers"
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "Python's headers"
+    return None
+
+
 def build_binding(force: bool = False) -> str:
     """Compile the Python module _paged_binding (host code only, against the
     installed Python's and PyTorch's headers)."""
     if not force and not stale(LIB_BINDING):
         return LIB_BINDING
-    import sysconfig
-
+    if binding_lacks():
+        raise RuntimeError(f"_paged_binding cannot be built without {binding_lacks()}")
     import torch
-    base = os.path.join(os.path.dirname(torch.__file__))
+    base = torch_dir()
     cuda = os.path.dirname(os.path.dirname(nvcc())) if os.path.isabs(nvcc()) else "/usr/local/cuda"
     tmp = LIB_BINDING + f".tmp{os.getpid()}"
     subprocess.check_call([
@@ -80,11 +103,8 @@ def build_binding(force: bool = False) -> str:
     return LIB_BINDING
 
 
-def build(force: bool = False, verbose: bool = False, check: bool = False) -> str:
-    """Compile libcswattn.so (or, with check, libcswattn_check.so: the same
-    library with CSWATTN_CHECK=1 device-side bounds checks), and the Python
-    module that makes the paged cache's calls."""
-    build_binding(force)
+def build_library(force: bool = False, verbose: bool = False, check: bool = False) -> str:
+    """Compile libcswattn.so (or, with check, libcswattn_check.so): nvcc alone."""
     lib = LIB_CHECK if check else LIB
     if not force and not stale(lib):
         return lib
@@ -96,6 +116,20 @@ def build(force: bool = False, verbose: bool = False, check: bool = False) -> st
         cmd.insert(1, "-Xptxas=-v")
     subprocess.check_call(cmd)
     os.replace(tmp, lib)
+    return lib
+
+
+def build(force: bool = False, verbose: bool = False, check: bool = False) -> str:
+    """Compile libcswattn.so (or, with check, libcswattn_check.so: the same
+    library with CSWATTN_CHECK=1 device-side bounds checks), and the Python
+    module that makes the paged cache's calls where it can be compiled: the
+    library is a C library, which needs neither Python nor PyTorch."""
+    lib = build_library(force, verbose, check)
+    if binding_lacks():
+        print(f"_paged_binding is not built, and the paged calls from Python are missing: no {binding_lacks()} here",
+              file=sys.stderr)
+    else:
+        build_binding(force)
     return lib
 
 
