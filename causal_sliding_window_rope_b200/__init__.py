@@ -405,12 +405,16 @@ def _paged_calls():
     library. Raises if it has not been built: there is no fallback."""
     global _paged
     if _paged is None:
-        import torch  # noqa: F401  (the module is linked against its libraries)
+        import torch  # (the module is linked against its libraries)
+
+        from .build import binding_id
+        rebuild = "build it with `python -m causal_sliding_window_rope_b200.build`"
         try:
             from . import _paged_binding as m
         except ImportError as e:
-            raise RuntimeError("_paged_binding.so is missing or does not fit this PyTorch; build it with "
-                               "`python -m causal_sliding_window_rope_b200.build`") from e
+            raise RuntimeError(f"_paged_binding.so is missing or does not fit this PyTorch; {rebuild}") from e
+        if m.built_for != binding_id(torch.__version__):
+            raise RuntimeError(f"found {m.built_for}, wanted {binding_id(torch.__version__)}; {rebuild}")
         L = lib()
         m.bind(CswattnError, *(ctypes.cast(f, ctypes.c_void_p).value for f in (
             L.attn_paged_append, L.attn_paged, L.attn_paged_weigh, L.attn_paged_select, L.attn_paged_move,

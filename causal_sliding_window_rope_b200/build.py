@@ -11,6 +11,7 @@ from __future__ import annotations
 import glob
 import importlib.util
 import os
+import re
 import subprocess
 import sys
 import sysconfig
@@ -52,6 +53,8 @@ def stale(lib: str | None = None) -> bool:
     lib = lib or LIB
     if not os.path.exists(lib):
         return True
+    if lib == LIB_BINDING and binding_id().encode() not in open(lib, "rb").read():
+        return True
     t = os.path.getmtime(lib)
     return any(os.path.getmtime(d) > t for d in (binding_deps() if lib == LIB_BINDING else deps()))
 
@@ -67,6 +70,21 @@ def torch_dir() -> str | None:
     except ValueError:
         return None
     return os.path.dirname(spec.origin) if spec and spec.origin else None
+
+
+def torch_version() -> str | None:
+    base = torch_dir()
+    if base is None:
+        return None
+    with open(os.path.join(base, "version.py")) as f:
+        found = re.search(r"""__version__ = ['"]([^'"]+)""", f.read())
+    return found.group(1) if found else None
+
+
+def binding_id(version: str | None = None) -> str:
+    """The PyTorch and the Python that the module is compiled for, which it
+    holds as a text."""
+    return f"_paged_binding for PyTorch {version or torch_version()} and Python {sys.version_info[0]}.{sys.version_info[1]}"
 
 
 def binding_lacks() -> str | None:
@@ -94,6 +112,7 @@ def build_binding(force: bool = False) -> str:
     tmp = LIB_BINDING + f".tmp{os.getpid()}"
     subprocess.check_call([
         os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+        f'-DBUILT_FOR="{binding_id()}"',
         f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
         "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(base, "include"),
         "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),

@@ -410,5 +410,7 @@ PyMODINIT_FUNC PyInit__paged_binding() {
     *x.to = PyUnicode_InternFromString(x.name);
     if (!*x.to) return nullptr;
   }
-  return PyModule_Create(&module);
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "built_for", BUILT_FOR) < 0) Py_CLEAR(m);
+  return m;
 }

@@ -46,3 +46,28 @@ def test_both_are_built(compiler):
                 raise subprocess.CalledProcessError(1, cmd)
             m.setattr(subprocess, "check_call", fail)
             cs_build.build_binding(force=True)
+
+
+def test_another_pytorch_makes_the_module_stale(monkeypatch):
+    """The module is compiled for one PyTorch and one Python, and says which."""
+    cs_build.build_binding()
+    assert not cs_build.stale(cs_build.LIB_BINDING)
+    with pytest.MonkeyPatch.context() as m:
+        m.setattr(cs_build, "torch_version", lambda: "1.2.3+other", raising=False)
+        assert cs_build.stale(cs_build.LIB_BINDING)
+    with pytest.MonkeyPatch.context() as m:
+        m.setattr(sys, "version_info", (3, 99, 0, "final", 0))
+        assert cs_build.stale(cs_build.LIB_BINDING)
+
+
+def test_a_module_for_another_pytorch_is_refused(monkeypatch):
+    import torch
+
+    import causal_sliding_window_rope_b200 as cs
+    cs_build.build()
+    monkeypatch.setattr(cs, "_paged", None)
+    cs._paged_calls()
+    monkeypatch.setattr(cs, "_paged", None)
+    monkeypatch.setattr(torch, "__version__", "1.2.3+other")
+    with pytest.raises(RuntimeError, match="1.2.3"):
+        cs._paged_calls()
