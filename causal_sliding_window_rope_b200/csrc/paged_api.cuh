@@ -174,7 +174,7 @@ struct WeighWorkspace {
   paged::Plan* plan;
   int* seqs;
   float* part;
-  int max_rows;  // query rows of a sequence that the kernel of few takes
+  int max_rows;  // query rows of a sequence that the kernel of few is compiled for
   bool tiles;    // a sequence may have more
   size_t bytes;
 };
@@ -220,11 +220,12 @@ cswattn_status launch_weigh_rows(const paged::WeighRowsParams& rp, const CUtenso
 // As launch_paged, for the row weights.
 template <int D>
 cswattn_status launch_weigh(const paged::WeighRowsParams& rp, const paged::WeighTileParams& tp, bool tiles,
-                            const CUtensorMap& mk, const CUtensorMap& mq, cudaStream_t st, bool prepare_only) {
+                            int max_rows, const CUtensorMap& mk, const CUtensorMap& mq, cudaStream_t st,
+                            bool prepare_only) {
   if (!tiles)
-    return rp.max_rows == 8    ? launch_weigh_rows<D, 1>(rp, mk, st, prepare_only)
-           : rp.max_rows == 16 ? launch_weigh_rows<D, 2>(rp, mk, st, prepare_only)
-                               : launch_weigh_rows<D, 4>(rp, mk, st, prepare_only);
+    return max_rows == 8    ? launch_weigh_rows<D, 1>(rp, mk, st, prepare_only)
+           : max_rows == 16 ? launch_weigh_rows<D, 2>(rp, mk, st, prepare_only)
+                            : launch_weigh_rows<D, 4>(rp, mk, st, prepare_only);
   if (prepare_only) return set_smem(paged::weigh_tile_kernel<D>, paged::WeighTileSmem<D>::kBytes);
   launch_pdl(paged::weigh_tile_kernel<D>, dim3(paged::kWeighRuns), dim3(paged::kWeighThreads),
              paged::WeighTileSmem<D>::kBytes, st, mq, mk, tp);
@@ -417,7 +418,6 @@ cswattn_status attn_paged_weigh(const cswattn_layer* layer, const cswattn_paged*
   rp.v = v;
   rp.scale_log2 = s.scale * 1.4426950408889634f;
   rp.unit = page_unit(v.page_size, w.tiles ? 128 : paged::kBlk);
-  rp.max_rows = w.max_rows;
   rp.q = static_cast<const __nv_bfloat16*>(q_out);
   rp.lse = lse;
   rp.weight = weight;
@@ -438,10 +438,10 @@ cswattn_status attn_paged_weigh(const cswattn_layer* layer, const cswattn_paged*
   if (w.tiles && (st = make_map_group(&mq, q_out, v.n_tokens, s.H, s.D, s.g, tp.tpt)) != CSWATTN_OK) return st;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const auto launch = s.D == 64 ? launch_weigh<64> : launch_weigh<128>;
-  if ((st = launch(rp, tp, w.tiles, mk, mq, cs, true)) != CSWATTN_OK) return st;
+  if ((st = launch(rp, tp, w.tiles, w.max_rows, mk, mq, cs, true)) != CSWATTN_OK) return st;
   {
     ScopedTiming tm(CSWATTN_K_DECODE, cs);
-    launch(rp, tp, w.tiles, mk, mq, cs, false);
+    launch(rp, tp, w.tiles, w.max_rows, mk, mq, cs, false);
   }
   return launched("paged weights launch");
 }

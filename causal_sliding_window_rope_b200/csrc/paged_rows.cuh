@@ -69,12 +69,10 @@ __device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
                  : "memory");
 }
 
-// Blocks of the rows that sequence s's tokens see; 0 when it has no query row
-// or more than hi_rows of them (another kernel's).
-__device__ __forceinline__ int visible_blocks(const View& v, const Seq& s, int hi_rows, int& first) {
-  const long long rows = static_cast<long long>(s.n) * v.g;
+// Blocks of the rows that sequence s's tokens see; 0 when it has none.
+__device__ __forceinline__ int visible_blocks(const View& v, const Seq& s, int& first) {
   first = max(0, s.L - v.W + 1) / kBlk;
-  if (s.n == 0 || rows > hi_rows) return 0;
+  if (s.n == 0) return 0;
   return (s.L + s.n - 1) / kBlk - first + 1;
 }
 
@@ -212,12 +210,12 @@ struct Walk {
 };
 
 // Sum of the blocks before each sequence, in shared memory; all threads call.
-__device__ __forceinline__ void fill_prefix(const View& v, int* pre, int hi_rows, bool report) {
+__device__ __forceinline__ void fill_prefix(const View& v, int* pre, bool report) {
   for (int b = threadIdx.x; b < v.B; b += blockDim.x) {
     Seq s;
     int first;
     seq_load(v, b, report, s);
-    pre[b + 1] = visible_blocks(v, s, hi_rows, first);
+    pre[b + 1] = visible_blocks(v, s, first);
   }
   if (threadIdx.x == 0) pre[0] = 0;
   __syncthreads();
@@ -265,7 +263,7 @@ __global__ void __launch_bounds__(32 * (kKeyGroups * MB + 1), 1)
   }
   pdl_wait();
   const int c = blockIdx.x;
-  fill_prefix(v, pre, 16 * MB, c == 0);
+  fill_prefix(v, pre, c == 0);
   __shared__ DealShared s_deal;
   const Deal deal = deal_out(v, pre, gridDim.x, c, &s_deal);
   if (deal.at >= deal.end) return;
@@ -287,7 +285,7 @@ __global__ void __launch_bounds__(32 * (kKeyGroups * MB + 1), 1)
       Seq s;
       int first;
       seq_load(v, w.b, false, s);
-      visible_blocks(v, s, 16 * MB, first);
+      visible_blocks(v, s, first);
       UnitPages up(v, w.b, s, first * kBlk + my_unit * p.unit, kBlk, p.unit);
       for (int t = w.t0; t < w.t1; ++t) {
         const int page = up.page(t, lane < boxes);
@@ -335,7 +333,7 @@ __global__ void __launch_bounds__(32 * (kKeyGroups * MB + 1), 1)
     Seq s;
     int first;
     seq_load(v, w.b, false, s);
-    visible_blocks(v, s, 16 * MB, first);
+    visible_blocks(v, s, first);
     const int rows = s.n * v.g;
     const int lo_seq = max(0, s.L - v.W + 1), end_seq = s.L + s.n;
     // Q rows as A fragments; a row past the last is zero.

@@ -569,7 +569,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps, TILES ? 4 : 1) join_kernel(co
     int first;
     Seq s;
     seq_load(v, b, false, s);
-    if (visible_blocks(v, s, p.rows, first) == 0 || inf.y <= 1) return;
+    if (visible_blocks(v, s, first) == 0 || inf.y <= 1) return;
     if (inf.x < 0 || inf.x >= 2 * kSMs || inf.y > kSMs - (inf.x >> 1)) return;
     for (int r = warp_id(); r < s.n * v.g; r += kJoinWarps)
       join_rows<D, 1, 8>(

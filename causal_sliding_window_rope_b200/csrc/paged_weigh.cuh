@@ -17,7 +17,7 @@
 //   weigh_tile_kernel   many: tcgen05, 128 cached rows x 128 query rows per
 //     product, two threads per cached row; bound by the exponentials (one per
 //     score on the MUFU unit, 57 % busy). 2213 tokens of 16 heads on 4 over
-//     11081 rows 64 us = 530 TFLOP/s.A call with a chunk runs it for its
+//     11081 rows 64 us = 530 TFLOP/s. A call with a chunk runs it for its
 //     single tokens too.
 #pragma once
 #include "paged_tile.cuh"
@@ -30,7 +30,7 @@ namespace paged {
 struct WeighRowsParams {
   View v;
   float scale_log2;
-  int unit, max_rows;
+  int unit;
   const __nv_bfloat16* q;
   const float* lse;
   float* weight;
@@ -57,7 +57,7 @@ struct WeighGroups {
   static constexpr int value = NT <= 2 ? 4 : 2;
 };
 
-// NT: products of 8 query rows (max_rows <= 8 NT).
+// NT: products of 8 query rows; a sequence has at most 8 NT (max_new times the heads of a group).
 template <int D, int NT>
 __global__ void __launch_bounds__(32 * (4 * WeighGroups<NT>::value + 1), 1)
     weigh_rows_kernel(const __grid_constant__ CUtensorMap tmK, const WeighRowsParams p) {
@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(32 * (4 * WeighGroups<NT>::value + 1), 1)
     fence_barrier_init();
   }
   pdl_wait();
-  fill_prefix(v, pre, p.max_rows, c == 0);
+  fill_prefix(v, pre, c == 0);
   const Deal deal = deal_out(v, pre, gridDim.x, c, nullptr);
   if (deal.at >= deal.end) return;
   Walk w(deal);
@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(32 * (4 * WeighGroups<NT>::value + 1), 1)
       Seq s;
       int first;
       seq_load(v, w.b, false, s);
-      visible_blocks(v, s, p.max_rows, first);
+      visible_blocks(v, s, first);
       UnitPages up(v, w.b, s, first * kBlk + my_unit * p.unit, kBlk, p.unit);
       for (int t = w.t0; t < w.t1; ++t) {
         const int page = up.page(t, lane < boxes);
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(32 * (4 * WeighGroups<NT>::value + 1), 1)
     Seq s;
     int first;
     seq_load(v, w.b, false, s);
-    visible_blocks(v, s, p.max_rows, first);
+    visible_blocks(v, s, first);
     const int rows = s.n * v.g, end = s.L + s.n;
     // Query rows as B fragments (column = row), their log-sum-exp and the cached rows they see.
     uint32_t qb[NT][D / 16][2];
