@@ -43,7 +43,9 @@ template <int D>
 struct WeighRowsSmem {
   static constexpr int kPanel = kBlk * 128;
   static constexpr int kStage = (D / 64) * kPanel;   // a block of K
-  static constexpr int kStages = D == 128 ? 12 : 16;
+  // (128 KB in flight on an SM; 12 slots at head_dim 128: step 12.5 -> 13.0 us,
+  // 32 sequences of 8192 rows alike)
+  static constexpr int kStages = D == 128 ? 8 : 16;
   static constexpr int kOffBar = kStages * kStage;
   static constexpr int kOffPre = kOffBar + 8 * (2 * kStages + 2);
   static constexpr int kBytes = kOffPre + 1024;      // and 4 (B + 1) more

@@ -120,7 +120,7 @@ def lengths(B, lo, hi, seed):
 
 FEW = [
     # B, lens, most new tokens, H, Hk, D, page, W, scale
-    (32, (1500, 4500), 1, 12, 4, 128, 64, None, 0.0),    # 3 query rows: 40 blocks a CTA, 3 turns of 12 slots
+    (32, (1500, 4500), 1, 12, 4, 128, 64, None, 0.0),    # 3 query rows: 40 blocks a CTA, 5 turns of 8 slots
     (32, (1500, 4500), 4, 12, 4, 128, 48, None, 0.0),    # 12
     (32, (1500, 4500), 8, 12, 4, 128, 16, None, 0.4),    # 24
     (32, (2500, 5500), 1, 12, 4, 64, 128, None, 0.0),    # 54 blocks a CTA, 3 turns of 16 slots
