@@ -184,7 +184,10 @@ struct WeighWorkspace {
 // of its sequences, single tokens too. Both launched, each for its sequences,
 // is the slower for 31 single tokens over 2000 rows beside a chunk of 512
 // tokens (38.2 us, 36.3) and for 8 sequences of 64 tokens (12.8, 10.8), the
-// faster for 63 single tokens over 4000 rows beside a chunk of 64 (79.9, 90.6).
+// faster for 63 single tokens over 4000 rows beside a chunk of 64 (79.9, 90.6)
+// and for 31 over 2000 beside one of 20 (30.8, 32.5): many long caches beside
+// a short chunk lose by it, short caches and long chunks gain, and the host,
+// which knows max_new alone, cannot tell them apart.
 WeighWorkspace carve_weigh(const Shape& s, const paged::View& v, void* base) {
   uint8_t* p = static_cast<uint8_t*>(base);
   WeighWorkspace w;

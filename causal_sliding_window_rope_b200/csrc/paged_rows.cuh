@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(32 * (kKeyGroups * MB + 1), 1)
         for (int nt = 0; nt < 2; ++nt) {
           const float p0 = ex2(sc[nt][2 * e] - mu), p1 = ex2(sc[nt][2 * e + 1] - mu);
           sum[e] += p0 + p1;
-          pa[nt * 2 + e] = pack_bf16x2(p0, p1);  // bf16 operand of the second product: half a step, 2^-9 of each weight
+          pa[nt * 2 + e] = pack_bf16x2(p0, p1);  // bf16 operand of the second product: half a step, 2^-8 of each weight
         }
       }
       ok = __all_sync(0xffffffffu, mbar_wait(&full_v[stage], use & 1, wc));

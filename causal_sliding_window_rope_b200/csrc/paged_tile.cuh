@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
               f2_unpack(x2, x0, x1);
               const float p0 = ex2(x0), p1 = ex2(x1);
               ls2[e & 3] = f2_add(ls2[e & 3], f2_pack(p0, p1));
-              pk[e] = pack_bf16x2(p0, p1);  // half a bf16 step, 2^-9 of each weight
+              pk[e] = pack_bf16x2(p0, p1);  // half a bf16 step, 2^-8 of each weight
             }
             tmem_st16(tS + q * 16, pk);
           }

@@ -13,10 +13,11 @@
 //   weigh_rows_kernel   few (<= 32): bound by reading K once and by the start
 //     of a CTA. Blocks of 64 cached rows, dealt out evenly as in the attention
 //     of few rows; mma.sync with K as the first operand, the query rows as
-//     columns (8 per product). 32 ragged sequences of up to 2048 rows 12.7 us.
+//     columns (8 per product). 32 ragged sequences of up to 2048 rows 12.5 us.
 //   weigh_tile_kernel   many: tcgen05, 128 cached rows x 128 query rows per
-//     product, two threads per cached row; bound by the exponentials (one per
-//     score on the MUFU unit, 57 % busy). 2213 tokens of 16 heads on 4 over
+//     product, two threads per cached row; no unit is saturated (the exponentials',
+//     one per score, is 55 % busy and would take 33 us alone, issue slots 46 %,
+//     the tensor pipe 24 %): a tile's chain of waits bounds it. 2213 tokens of 16 heads on 4 over
 //     11081 rows 64 us = 530 TFLOP/s. A call with a chunk runs it for its
 //     single tokens too.
 #pragma once
