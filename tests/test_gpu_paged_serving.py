@@ -60,7 +60,7 @@ def test_tokens_of_a_sequence_beside_one_that_does_not_fit(start, max_new):
 
 
 def test_the_documented_loop():
-    """README's serving loop, word for word: prompts' chunks beside single tokens, then generation until rows go."""
+    """The documented serving loop, word for word: prompts' chunks beside single tokens, then generation until rows go."""
     readme = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")).read()
     code = re.search(r"A serving loop over a paged cache.*?```python\n(.*?)```", readme, re.S).group(1)
     g = torch.Generator(device="cuda").manual_seed(71)
